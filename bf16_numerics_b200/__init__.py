@@ -29,7 +29,8 @@ STABILIZED_MARGIN = _abi.FA_SOFTMAX_STABILIZED_MARGIN
 __all__ = ["FaError", "STANDARD", "STABILIZED", "STABILIZED_MARGIN", "RowStats", "fa_fwd", "fa_bwd", "fa_fwd_o_hp", "fa_bwd_o_hp", "fa_bwd_workspace_bytes",
            "fa_bwd_workspace_offsets", "fa_status_string", "fa_device_error", "fa_timing_enable",
            "fa_timing_read", "fa_debug_set_wait_limit_ns", "fa_debug_inject_stall", "attention_forward",
-           "attention_backward", "library_path"]
+           "attention_backward", "library_path", "NO_WINDOW", "fa_window_fwd", "fa_window_bwd",
+           "fa_window_bwd_workspace_bytes", "window_attention_forward", "window_attention_backward"]
 
 
 class FaError(RuntimeError):
@@ -241,4 +242,134 @@ def attention_backward(q, k, v, o, dO, lse, row_m, causal: bool = True, softmax_
         workspace = torch.empty(fa_bwd_workspace_bytes(B, H, N, d), device=q.device, dtype=torch.uint8)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd(q, k, v, o, dO, lse, row_m, dq, dk, dv, workspace, causal, softmax_mode, beta, stream)
+    return dq, dk, dv, workspace
+
+
+# ------------------------------------------------- sliding window with sinks
+
+#: a window that hides nothing: plain causal attention
+NO_WINDOW = 2**31 - 1
+
+
+def _call(device, stream, fn, *args):
+    """fn(*args, stream handle) on `stream` (default: the device's current one) with `device` current."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, stream.cuda_stream)
+    with torch.cuda.device(device):
+        return fn(*args, stream.cuda_stream)
+
+
+def _device_of(q):
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dim() != 4 or not q.is_cuda:
+        raise ValueError("q must be a CUDA bfloat16 tensor [B, H, N, d]")
+    return q.device
+
+
+def _view(name, t, shape, device):
+    """fa_view of a bf16 tensor of that shape on that device whose last axis is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16 or t.device != device or t.shape != shape:
+        raise ValueError(f"{name} must be a bfloat16 tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous (strides {s})")
+    return ctypes.byref(_abi.FaView(t.data_ptr(), s[0], s[1], s[2]))
+
+
+def _vec(name, t, shape, device, dtype=torch.float32):
+    """data pointer of a contiguous tensor of that shape, type and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _window_stats(stats, rows, device):
+    if stats is None:
+        return None
+    ptrs = [None if getattr(stats, n) is None else
+            _vec(f"stats.{n}", getattr(stats, n), rows, device, torch.int32 if n == "rs" else torch.float32)
+            for n in ("rm", "rs", "m", "pbar_max")]
+    return ctypes.byref(_abi.FaRowStats(*ptrs))
+
+
+def fa_window_fwd(q, k, v, o, lse, stats: RowStats | None = None, window: int = NO_WINDOW, sinks: int = 0,
+                  softmax_mode: int = STABILIZED, beta: float = 2.0, stream=None) -> None:
+    """C ``fa_window_fwd``: causal attention over the last ``window`` keys and the first ``sinks``.
+
+    q, o [B, H, N, d] and k, v [B, Hkv, N, d] are bfloat16 tensors of any strides the header's ``fa_view`` allows
+    (H a multiple of Hkv); lse and the statistics are contiguous [B, H, N]."""
+    device = _device_of(q)
+    B, H, N, d = q.shape
+    Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else -1
+    kv = (B, Hkv, N, d)
+    code = _call(device, stream, _abi.load().fa_window_fwd, _view("q", q, q.shape, device), _view("k", k, kv, device),
+                 _view("v", v, kv, device), _view("o", o, q.shape, device), _vec("lse", lse, (B, H, N), device),
+                 _window_stats(stats, (B, H, N), device), B, H, Hkv, N, d, window, sinks, softmax_mode, beta)
+    if code != _abi.FA_OK:
+        raise FaError(code, "fa_window_fwd")
+
+
+def fa_window_bwd_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int, window: int = NO_WINDOW,
+                                  sinks: int = 0) -> int:
+    return int(_abi.load().fa_window_bwd_workspace_bytes(B, H, Hkv, N, d, window, sinks))
+
+
+def fa_window_bwd(q, k, v, o, dO, lse, row_m, dq, dk, dv, workspace, window: int = NO_WINDOW, sinks: int = 0,
+                  softmax_mode: int = STABILIZED, beta: float = 2.0, stream=None) -> None:
+    """C ``fa_window_bwd``: writes dq [B, H, N, d], dk and dv [B, Hkv, N, d]; workspace is a uint8 CUDA tensor."""
+    device = _device_of(q)
+    B, H, N, d = q.shape
+    Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else -1
+    kv = (B, Hkv, N, d)
+    code = _call(device, stream, _abi.load().fa_window_bwd, _view("q", q, q.shape, device), _view("k", k, kv, device),
+                 _view("v", v, kv, device), _view("o", o, q.shape, device), _view("dO", dO, q.shape, device),
+                 _vec("lse", lse, (B, H, N), device),
+                 None if row_m is None else _vec("row_m", row_m, (B, H, N), device), _view("dq", dq, q.shape, device),
+                 _view("dk", dk, kv, device), _view("dv", dv, kv, device),
+                 _vec("workspace", workspace, (workspace.numel(),), device, torch.uint8), workspace.numel(),
+                 B, H, Hkv, N, d, window, sinks, softmax_mode, beta)
+    if code != _abi.FA_OK:
+        raise FaError(code, "fa_window_bwd")
+
+
+def _allocate_on(stream):
+    """Context in which new tensors belong to `stream` (None: the current one)."""
+    return torch.cuda.stream(stream)
+
+
+def window_attention_forward(q, k, v, window: int = NO_WINDOW, sinks: int = 0, softmax_mode: int = STABILIZED,
+                             beta: float = 2.0, with_stats: bool = True, stream=None):
+    """Allocate outputs (torch; o strided like q) and run fa_window_fwd.  Returns (o, lse, stats)."""
+    device = _device_of(q)
+    B, H, N, _ = q.shape
+    with _allocate_on(stream):
+        o = torch.empty_like(q)
+        lse = torch.empty(B, H, N, device=device, dtype=torch.float32)
+        stats = RowStats.empty(B, H, N, device) if with_stats else None
+    fa_window_fwd(q, k, v, o, lse, stats, window, sinks, softmax_mode, beta, stream)
+    return o, lse, stats
+
+
+def window_attention_backward(q, k, v, o, dO, lse, row_m, window: int = NO_WINDOW, sinks: int = 0,
+                              softmax_mode: int = STABILIZED, beta: float = 2.0, workspace=None, stream=None):
+    """Allocate gradients (torch; strided like q, k, v) and run fa_window_bwd.  Returns (dq, dk, dv, workspace)."""
+    device = _device_of(q)
+    B, H, N, d = q.shape
+    with _allocate_on(stream):
+        if workspace is None:
+            workspace = torch.empty(fa_window_bwd_workspace_bytes(B, H, k.shape[1], N, d, window, sinks),
+                                    device=device, dtype=torch.uint8)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    fa_window_bwd(q, k, v, o, dO, lse, row_m, dq, dk, dv, workspace, window, sinks, softmax_mode, beta, stream)
     return dq, dk, dv, workspace

@@ -38,12 +38,18 @@ KERNEL_NAMES = ("fa_fwd_kernel", "fa_bwd_delta_kernel", "fa_bwd_main_kernel", "f
 EXPORTS = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_bwd_workspace_delta_offset",
            "fa_bwd_workspace_dq_offset", "fa_status_string", "fa_device_error", "fa_timing_enable",
            "fa_timing_read", "fa_bwd_noalloc", "fa_last_error_string", "fa_fwd_o_hp", "fa_bwd_o_hp",
-           "fa_debug_set_wait_limit_ns", "fa_debug_inject_stall")
+           "fa_debug_set_wait_limit_ns", "fa_debug_inject_stall", "fa_window_fwd", "fa_window_bwd",
+           "fa_window_bwd_workspace_bytes")
 
 
 class FaRowStats(ctypes.Structure):
     _fields_ = [("rm", ctypes.c_void_p), ("rs", ctypes.c_void_p), ("m", ctypes.c_void_p),
                 ("pbar_max", ctypes.c_void_p)]
+
+
+class FaView(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
+                ("stride_n", ctypes.c_longlong)]
 
 
 _lib = None
@@ -68,6 +74,13 @@ def load() -> ctypes.CDLL:
     for name in ("fa_bwd_workspace_bytes", "fa_bwd_workspace_delta_offset", "fa_bwd_workspace_dq_offset"):
         getattr(lib, name).argtypes = [i, i, i, i]
         getattr(lib, name).restype = sz
+    view = ctypes.POINTER(FaView)
+    lib.fa_window_fwd.argtypes = [view] * 4 + [vp, ctypes.POINTER(FaRowStats)] + [i] * 8 + [f, vp]
+    lib.fa_window_fwd.restype = i
+    lib.fa_window_bwd.argtypes = [view] * 5 + [vp, vp] + [view] * 3 + [vp, sz] + [i] * 8 + [f, vp]
+    lib.fa_window_bwd.restype = i
+    lib.fa_window_bwd_workspace_bytes.argtypes = [i] * 7
+    lib.fa_window_bwd_workspace_bytes.restype = sz
     lib.fa_status_string.argtypes = [i]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_last_error_string.argtypes = []

@@ -222,4 +222,19 @@ struct BwdParams {
   float scale;
 };
 
+// Element strides of a bf16 array [B, H, N, d] whose last axis is contiguous.
+struct ViewStrides {
+  long long b, h, n;
+};
+// The windowed forms of the main kernels (WIN): an item is a 128-key block of
+// one *key* head, and its query blocks are those that see its keys, of every
+// query head that shares it, one head after the other -- so dK and dV of a
+// shared head are summed in the accumulators.  BH counts key heads (B * Hkv).
+struct BwdWinParams : BwdParams {
+  WindowShape w;
+  ViewStrides dk_strides, dv_strides;
+};
+template <bool WIN>
+using BwdArgs = std::conditional_t<WIN, BwdWinParams, BwdParams>;
+
 }  // namespace fa

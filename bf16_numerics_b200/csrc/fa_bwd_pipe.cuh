@@ -105,10 +105,14 @@ __device__ __forceinline__ void tma_reduce_add_3d(const void* tmap, uint32_t src
 // r*G + G-1-c (r odd) of the list sorted by decreasing work (key block 0
 // first when causal), G = gridDim.x.  Item number w is key block w / BH of
 // batch*head w % BH.  The cursor walks (item, query block) pairs in order.
+template <bool WIN>
 struct BwdCursor {
   int c, G, W, BH, n_blk, causal;
   int r, kblk, bh, n, i0, i;
   bool valid;
+  // WIN: the window, query blocks per head, flat index of the first query head
+  std::conditional_t<WIN, WindowShape, int> win;
+  int nq, bh0;
   __device__ __forceinline__ void load() {
     const int w = r * G + ((r & 1) ? (G - 1 - c) : c);
     valid = w < W;
@@ -118,9 +122,28 @@ struct BwdCursor {
       n = causal ? (n_blk - kblk) : n_blk;
       i0 = causal ? kblk : 0;
       i = 0;
+      if constexpr (WIN) {
+        nq = win.last_query_block(kblk, n_blk) - kblk + 1;
+        n = nq * win.G;
+        bh0 = bh * win.G;  // B-major: flat key head b * Hkv + hk -> flat query head b * H + hk * G
+      }
     }
   }
-  __device__ __forceinline__ void start(const BwdParams& p) {
+  // query block and flat query head of the item's step k
+  __device__ __forceinline__ int qblk_of(int k) const {
+    if constexpr (WIN)
+      return i0 + k % nq;
+    else
+      return i0 + k;
+  }
+  __device__ __forceinline__ int head_of(int k) const {
+    if constexpr (WIN)
+      return bh0 + k / nq;
+    else
+      return bh;
+  }
+  __device__ __forceinline__ void start(const BwdArgs<WIN>& p) {
+    if constexpr (WIN) win = p.w;
     c = blockIdx.x;
     G = gridDim.x;
     BH = p.BH;
@@ -140,15 +163,18 @@ struct BwdCursor {
     ++r;
     load();
   }
-  __device__ __forceinline__ int qblk() const { return i0 + i; }
+  __device__ __forceinline__ int qblk() const { return qblk_of(i); }
+  __device__ __forceinline__ int head() const { return head_of(i); }
 };
 
+template <bool WIN = false>
 __global__ void __launch_bounds__(512, 1)
 fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                         const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_dk,
-                        const __grid_constant__ CUtensorMap tm_dv, const BwdParams p) {
+                        const __grid_constant__ CUtensorMap tm_dv, const BwdArgs<WIN> p) {
   using L = BwdPipeLayout;
+  using Cursor = BwdCursor<WIN>;
   constexpr int TILE = L::TILE, NST = L::NST;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -226,7 +252,7 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
       tma_prefetch_desc(&tm_do);
-      BwdCursor cur;
+      Cursor cur;
       cur.start(p);
       int g = 0, last_r = -1;
       int issued[NST];
@@ -234,10 +260,16 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
       auto load_q = [&](int i, int gq) {
         const int s = gq % NST, use = gq / NST;
         if (use > 0 && !wait(bar(L::Q_EMPTY + s), (use - 1) & 1, 1)) return false;
-        const int row0 = (cur.i0 + i) * L::B;
+        const int row0 = cur.qblk_of(i) * L::B;
         mbar_expect_tx(bar(L::Q_FULL + s), 2 * TILE);
-        tma_load_3d(base + L::Q_OFF + s * TILE, &tm_q, bar(L::Q_FULL + s), 0, row0, cur.bh);
-        tma_load_3d(base + L::DO_OFF + s * TILE, &tm_do, bar(L::Q_FULL + s), 0, row0, cur.bh);
+        if constexpr (WIN) {
+          const int f = cur.head_of(i), b = f / p.w.H, h = f - b * p.w.H;
+          tma_load_4d(base + L::Q_OFF + s * TILE, &tm_q, bar(L::Q_FULL + s), 0, row0, h, b);
+          tma_load_4d(base + L::DO_OFF + s * TILE, &tm_do, bar(L::Q_FULL + s), 0, row0, h, b);
+        } else {
+          tma_load_3d(base + L::Q_OFF + s * TILE, &tm_q, bar(L::Q_FULL + s), 0, row0, cur.bh);
+          tma_load_3d(base + L::DO_OFF + s * TILE, &tm_do, bar(L::Q_FULL + s), 0, row0, cur.bh);
+        }
         issued[s] = gq;
         return true;
       };
@@ -252,8 +284,14 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         if (!ok) break;
         if (cur.r > 0 && !wait(bar(L::KV_EMPTY), (cur.r - 1) & 1, 1)) break;
         mbar_expect_tx(bar(L::KV_FULL), 2 * TILE);
-        tma_load_3d(base + L::K_OFF, &tm_k, bar(L::KV_FULL), 0, cur.kblk * L::B, cur.bh);
-        tma_load_3d(base + L::V_OFF, &tm_v, bar(L::KV_FULL), 0, cur.kblk * L::B, cur.bh);
+        if constexpr (WIN) {
+          const int hkv = p.w.H / p.w.G, b = cur.bh / hkv, hk = cur.bh - b * hkv;
+          tma_load_4d(base + L::K_OFF, &tm_k, bar(L::KV_FULL), 0, cur.kblk * L::B, hk, b);
+          tma_load_4d(base + L::V_OFF, &tm_v, bar(L::KV_FULL), 0, cur.kblk * L::B, hk, b);
+        } else {
+          tma_load_3d(base + L::K_OFF, &tm_k, bar(L::KV_FULL), 0, cur.kblk * L::B, cur.bh);
+          tma_load_3d(base + L::V_OFF, &tm_v, bar(L::KV_FULL), 0, cur.kblk * L::B, cur.bh);
+        }
         last_r = cur.r;
         if (cur.r == 0 && (!wait(bar(L::KV_FULL), 0, 23) || !wait(bar(L::Q_FULL), 0, 24))) break;
         for (int i = first; ok && i < cur.n; ++i) ok = load_q(i, g + i);
@@ -293,7 +331,7 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
           mma_ss2(tmem + L::DPT_COL, lo_k + (L::V_OFF >> 4) + 2u * ks, HI, ob + 2u * ks, HI, IDESC_SQ, ks > 0 ? 1u : 0u);
         tc_commit(bar(L::DP_FULL));
       };
-      BwdCursor cur;
+      Cursor cur;
       cur.start(p);
       int g0 = 0;
       bool ok = true;
@@ -376,12 +414,12 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     struct Vec3 {
       float lse, m, dl;
     };
-    auto load_vec = [&](const BwdCursor& c) {
+    auto load_vec = [&](const Cursor& c) {
       Vec3 v{0.f, 0.f, 0.f};
       if (c.valid) {
         const int q = c.qblk() * L::B + t;
         if (q < p.N) {
-          const size_t vi = static_cast<size_t>(c.bh) * p.N + q;
+          const size_t vi = static_cast<size_t>(c.head()) * p.N + q;
           v.lse = __ldg(p.lse + vi);
           v.dl = __ldg(p.delta + vi);
           v.m = (p.mode == 1) ? __ldg(p.row_m + vi) : 0.f;
@@ -389,7 +427,7 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
       }
       return v;
     };
-    auto publish_vec = [&](int g, const BwdCursor& c, const Vec3& v) {
+    auto publish_vec = [&](int g, const Cursor& c, const Vec3& v) {
       const int s = g & 1, q = c.qblk() * L::B + t;
       float na = -INFINITY, dl = 0.f;
       if (q < p.N) {
@@ -405,7 +443,7 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     };
     grid_dependency_wait();  // delta and the cleared dQ accumulator: the delta grid's
     // pub walks two blocks ahead of cur, nxt holds the loads for pub
-    BwdCursor cur, pub;
+    Cursor cur, pub;
     cur.start(p);
     pub.start(p);
     int g_pub = 0;
@@ -464,7 +502,7 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         fence_proxy_async_smem();
         named_barrier_sync(2, 128);
         if (t == 0) {
-          tma_reduce_add_3d(&tm_dq, base + L::DQS_OFF, 32 * half, q0, cur.bh);
+          tma_reduce_add_3d(&tm_dq, base + L::DQS_OFF, 32 * half, q0, cur.head());
           bulk_commit();
         }
       }
@@ -486,7 +524,7 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     const uint64_t C2 = f2_pack(c_log2, c_log2);
     const int qoff = 64 * h;
     const uint32_t ds_row = base + L::DS_OFF + h * TILE + t * 128;
-    BwdCursor cur;
+    Cursor cur;
     cur.start(p);
     int g = 0;
     // Error discipline: the eight warps meet on named barrier 1 once per item,
@@ -507,7 +545,16 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         tc_fence_after();
         const uint32_t va = base + L::VEC_OFF + ((b * 2 + 0) * 128 + 64 * h) * 4;
         const uint32_t vd = base + L::VEC_OFF + ((b * 2 + 1) * 128 + 64 * h) * 4;
-        const bool diag = p.causal && (cur.i0 + i == cur.kblk);
+        const bool diag = !WIN && p.causal && (cur.i0 + i == cur.kblk);
+        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};  // WIN: queries of this half that see key t
+        bool part = false;                             // WIN: some pair of the two blocks is hidden
+        if constexpr (WIN) {
+          const int qb = cur.qblk_of(i);
+          part = !p.w.block_full(qb, cur.kblk);
+          const RowMask mk = p.w.column_mask(cur.kblk * L::B + t, qb * L::B + qoff);
+          vis[0] = mk.word(0);
+          vis[1] = mk.word(32);
+        }
         uint64_t p2[32];  // this row's 64 P values (fp32 pairs)
         uint32_t rs1[32];  // S^T columns 32-63, loading while the first half is computed
         {
@@ -544,6 +591,13 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             if (t > qg + 1) p1 = 0.f;
             if (t > qg + 2) p2v = 0.f;
             if (t > qg + 3) p3 = 0.f;
+          }
+          if (WIN && part) {
+            const uint32_t v = vis[ql >> 5] >> (ql & 31);
+            if (!(v & 1u)) p0 = 0.f;
+            if (!(v & 2u)) p1 = 0.f;
+            if (!(v & 4u)) p2v = 0.f;
+            if (!(v & 8u)) p3 = 0.f;
           }
           p2[pi] = f2_pack(p0, p1);
           p2[pi + 1] = f2_pack(p2v, p3);
@@ -636,8 +690,13 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
       fence_proxy_async_smem();
       if (!named_barrier_and(1, 256, ok)) break;
       if (t == 0) {
-        tma_store_3d(h == 0 ? static_cast<const void*>(&tm_dv) : static_cast<const void*>(&tm_dk),
-                     base + L::DS_OFF + h * TILE, 0, cur.kblk * L::B, cur.bh);
+        const void* map = h == 0 ? static_cast<const void*>(&tm_dv) : static_cast<const void*>(&tm_dk);
+        if constexpr (WIN) {
+          const int hkv = p.w.H / p.w.G, b = cur.bh / hkv;
+          tma_store_4d(map, base + L::DS_OFF + h * TILE, 0, cur.kblk * L::B, cur.bh - b * hkv, b);
+        } else {
+          tma_store_3d(map, base + L::DS_OFF + h * TILE, 0, cur.kblk * L::B, cur.bh);
+        }
         bulk_commit();
         bulk_wait_read_all();  // the tile is the next item's dS tile
       }

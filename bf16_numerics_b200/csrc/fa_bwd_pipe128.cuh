@@ -118,13 +118,15 @@ __device__ __forceinline__ void bwd_item_decode(const BwdParams& p, int w, int& 
 // workspace (so CTAs that finish early take more items) and publishes it, one
 // item ahead of its own loads, in a ring of shared-memory slots; every other
 // role reads its items from the ring.  Same interface as BwdCursor.
+template <bool WIN>
 struct RingCursor {
   BoundedWait wt;
   uint32_t ring, full, empty;  // shared addresses: slot array, ITEM_FULL[0], ITEM_EMPTY[0]
   bool uniform;                // called by whole warps (warp-uniform waits)
-  BwdParams p;
+  BwdArgs<WIN> p;
   int r, kblk, bh, n, i0, i;
   bool valid;
+  int nq;  // WIN: query blocks per query head
   __device__ __forceinline__ void load() {
     const int slot = r & 3;
     const bool got = uniform ? wt.warp(full + 8u * slot, (r >> 2) & 1, 40) : wt(full + 8u * slot, (r >> 2) & 1, 40);
@@ -138,7 +140,24 @@ struct RingCursor {
     n = p.causal ? (p.n_blk - kblk) : p.n_blk;
     i0 = p.causal ? kblk : 0;
     i = 0;
+    if constexpr (WIN) {
+      nq = p.w.last_query_block(kblk, p.n_blk) - kblk + 1;
+      n = nq * p.w.G;
+    }
     valid = true;
+  }
+  // query block and flat query head of the item's step k (as in BwdCursor)
+  __device__ __forceinline__ int qblk_of(int k) const {
+    if constexpr (WIN)
+      return i0 + k % nq;
+    else
+      return i0 + k;
+  }
+  __device__ __forceinline__ int head_of(int k) const {
+    if constexpr (WIN)
+      return bh * p.w.G + k / nq;
+    else
+      return bh;
   }
   __device__ __forceinline__ void start() {
     r = 0;
@@ -158,14 +177,17 @@ struct RingCursor {
     ++r;
     load();
   }
-  __device__ __forceinline__ int qblk() const { return i0 + i; }
+  __device__ __forceinline__ int qblk() const { return qblk_of(i); }
+  __device__ __forceinline__ int head() const { return head_of(i); }
 };
 
+template <bool WIN = false>
 __global__ void __launch_bounds__(512, 1)
 fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
-                           const __grid_constant__ CUtensorMap tm_dq, const BwdParams p) {
+                           const __grid_constant__ CUtensorMap tm_dq, const BwdArgs<WIN> p) {
   using L = BwdPipe128Layout;
+  using Cursor = RingCursor<WIN>;
   constexpr int TILE = L::TILE, HALF = L::HALF, NST = L::NST;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -240,6 +262,7 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       struct PItem {
         int r, kblk, bh, n, i0;
         bool valid;
+        int nq;
       };
       const int W = p.n_blk * p.BH;
       auto publish = [&](int r, PItem& it) -> bool {
@@ -255,6 +278,10 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
           bwd_item_decode(p, v, it.kblk, it.bh);
           it.n = p.causal ? (p.n_blk - it.kblk) : p.n_blk;
           it.i0 = p.causal ? it.kblk : 0;
+          if constexpr (WIN) {
+            it.nq = p.w.last_query_block(it.kblk, p.n_blk) - it.kblk + 1;
+            it.n = it.nq * p.w.G;
+          }
         }
         return true;
       };
@@ -265,12 +292,20 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       auto load_q = [&](int i, int gq) {
         const int s = gq % NST, use = gq / NST;
         if (use > 0 && !wait(bar(L::Q_EMPTY + s), (use - 1) & 1, 1)) return false;
-        const int row0 = (cur.i0 + i) * L::B;
+        const int row0 = (WIN ? cur.i0 + i % cur.nq : cur.i0 + i) * L::B;
         const uint32_t qd = base + L::Q_OFF + s * TILE, dod = base + L::DO_OFF + s * TILE;
         mbar_expect_tx(bar(L::Q_FULL + s), 2 * TILE);
-        for (int h = 0; h < 2; ++h) {
-          tma_load_3d(qd + h * HALF, &tm_q, bar(L::Q_FULL + s), 64 * h, row0, cur.bh);
-          tma_load_3d(dod + h * HALF, &tm_do, bar(L::Q_FULL + s), 64 * h, row0, cur.bh);
+        if constexpr (WIN) {
+          const int f = cur.bh * p.w.G + i / cur.nq, b = f / p.w.H, hd = f - b * p.w.H;
+          for (int h = 0; h < 2; ++h) {
+            tma_load_4d(qd + h * HALF, &tm_q, bar(L::Q_FULL + s), 64 * h, row0, hd, b);
+            tma_load_4d(dod + h * HALF, &tm_do, bar(L::Q_FULL + s), 64 * h, row0, hd, b);
+          }
+        } else {
+          for (int h = 0; h < 2; ++h) {
+            tma_load_3d(qd + h * HALF, &tm_q, bar(L::Q_FULL + s), 64 * h, row0, cur.bh);
+            tma_load_3d(dod + h * HALF, &tm_do, bar(L::Q_FULL + s), 64 * h, row0, cur.bh);
+          }
         }
         issued[s] = gq;
         return true;
@@ -289,9 +324,17 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         if (!ok) break;
         if (cur.r > 0 && !wait(bar(L::KV_EMPTY), (cur.r - 1) & 1, 1)) break;
         mbar_expect_tx(bar(L::KV_FULL), 2 * TILE);
-        for (int h = 0; h < 2; ++h) {
-          tma_load_3d(base + L::K_OFF + h * HALF, &tm_k, bar(L::KV_FULL), 64 * h, cur.kblk * L::B, cur.bh);
-          tma_load_3d(base + L::V_OFF + h * HALF, &tm_v, bar(L::KV_FULL), 64 * h, cur.kblk * L::B, cur.bh);
+        if constexpr (WIN) {
+          const int hkv = p.w.H / p.w.G, b = cur.bh / hkv, hk = cur.bh - b * hkv;
+          for (int h = 0; h < 2; ++h) {
+            tma_load_4d(base + L::K_OFF + h * HALF, &tm_k, bar(L::KV_FULL), 64 * h, cur.kblk * L::B, hk, b);
+            tma_load_4d(base + L::V_OFF + h * HALF, &tm_v, bar(L::KV_FULL), 64 * h, cur.kblk * L::B, hk, b);
+          }
+        } else {
+          for (int h = 0; h < 2; ++h) {
+            tma_load_3d(base + L::K_OFF + h * HALF, &tm_k, bar(L::KV_FULL), 64 * h, cur.kblk * L::B, cur.bh);
+            tma_load_3d(base + L::V_OFF + h * HALF, &tm_v, bar(L::KV_FULL), 64 * h, cur.kblk * L::B, cur.bh);
+          }
         }
         last_r = cur.r;
         if (cur.r == 0 && (!wait(bar(L::KV_FULL), 0, 23) || !wait(bar(L::Q_FULL), 0, 24))) break;
@@ -343,7 +386,7 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         }
         tc_commit(bar(L::DP_FULL));
       };
-      RingCursor cur{wait, base + L::RING_OFF, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), false, p};
+      Cursor cur{wait, base + L::RING_OFF, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), false, p};
       cur.start();
       int g = 0;
       bool ok = true;
@@ -414,7 +457,7 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float scale = p.scale;
     if (t == 0) tma_prefetch_desc(&tm_dq);
-    RingCursor cur{wait, base + L::RING_OFF, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), true, p};
+    Cursor cur{wait, base + L::RING_OFF, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), true, p};
     cur.start();
     // A bounded wait that gives up only clears `ok`; the warpgroup leaves the
     // loop together at the AND vote on named barrier 2.
@@ -446,8 +489,8 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       fence_proxy_async_smem();
       if (!named_barrier_and(2, 128, ok)) break;
       if (t == 0) {
-        tma_reduce_add_3d(&tm_dq, box0, 0, q0, cur.bh);
-        tma_reduce_add_3d(&tm_dq, box1, 32, q0, cur.bh);
+        tma_reduce_add_3d(&tm_dq, box0, 0, q0, cur.head());
+        tma_reduce_add_3d(&tm_dq, box1, 32, q0, cur.head());
         bulk_commit();
       }
       // columns [64,128); then dP^T of the next block may overwrite them
@@ -461,8 +504,8 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       fence_proxy_async_smem();
       named_barrier_sync(2, 128);
       if (t == 0) {
-        tma_reduce_add_3d(&tm_dq, box0, 64, q0, cur.bh);
-        tma_reduce_add_3d(&tm_dq, box1, 96, q0, cur.bh);
+        tma_reduce_add_3d(&tm_dq, box0, 64, q0, cur.head());
+        tma_reduce_add_3d(&tm_dq, box1, 96, q0, cur.head());
         bulk_commit();
         bulk_wait_read_all();
         mbar_arrive(bar(L::DSTILE_FREE));  // the elementwise warps may write dS again
@@ -491,7 +534,7 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
     // threads t < 64 the exponent offset, threads t >= 64 delta.  The
     // raw values are loaded one block ahead (cursor pf).
     const int vq = t & 63, vrole = t >> 6;
-    RingCursor pf{wait, base + L::RING_OFF, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), true, p};
+    Cursor pf{wait, base + L::RING_OFF, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), true, p};
     pf.start();
     auto fetch = [&](float& x, float& y) {
       x = 0.f;
@@ -499,7 +542,7 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       if (pf.valid) {
         const int q = pf.qblk() * L::B + qoff + vq;
         if (q < p.N) {
-          const size_t vi = static_cast<size_t>(pf.bh) * p.N + q;
+          const size_t vi = static_cast<size_t>(pf.head()) * p.N + q;
           if (vrole == 0) {
             x = __ldg(p.lse + vi);
             y = mode1 ? __ldg(p.row_m + vi) : 0.f;
@@ -514,7 +557,7 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
     };
     float nx, ny;
     fetch(nx, ny);
-    RingCursor cur{wait, base + L::RING_OFF, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), true, p};
+    Cursor cur{wait, base + L::RING_OFF, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), true, p};
     cur.start();
     int g = 0;
     // Error discipline as in the d = 64 kernel: the two warpgroups meet on
@@ -546,7 +589,16 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         fetch(nx, ny);
         ok = ok && wait.warp(bar(L::S_FULL), g & 1, 9);
         tc_fence_after();
-        const bool diag = p.causal && (cur.i0 + i == cur.kblk);
+        const bool diag = !WIN && p.causal && (cur.i0 + i == cur.kblk);
+        uint32_t vis[2] = {0xffffffffu, 0xffffffffu};  // WIN: queries of this half that see key t
+        bool part = false;                             // WIN: some pair of the two blocks is hidden
+        if constexpr (WIN) {
+          const int qb = cur.qblk_of(i);
+          part = !p.w.block_full(qb, cur.kblk);
+          const RowMask mk = p.w.column_mask(cur.kblk * L::B + t, qb * L::B + qoff);
+          vis[0] = mk.word(0);
+          vis[1] = mk.word(32);
+        }
         uint64_t p2[32];  // this row's 64 P values (fp32 pairs)
         {
           uint32_t r0[32], r1[32];
@@ -584,6 +636,13 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
             if (t > qg + 1) p1 = 0.f;
             if (t > qg + 2) p2v = 0.f;
             if (t > qg + 3) p3 = 0.f;
+          }
+          if (WIN && part) {
+            const uint32_t v = vis[ql >> 5] >> (ql & 31);
+            if (!(v & 1u)) p0 = 0.f;
+            if (!(v & 2u)) p1 = 0.f;
+            if (!(v & 4u)) p2v = 0.f;
+            if (!(v & 8u)) p3 = 0.f;
           }
           p2[pi] = f2_pack(p0, p1);
           p2[pi + 1] = f2_pack(p2v, p3);
@@ -648,7 +707,14 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       const uint32_t col = (h == 0) ? L::DV_COL : L::DK_COL;
       const int key = cur.kblk * L::B + t;
       const bool row_ok = ok && key < p.N;
-      __nv_bfloat16* dst = (h == 0 ? p.dv : p.dk) + (static_cast<size_t>(cur.bh) * p.N + (row_ok ? key : 0)) * L::D;
+      __nv_bfloat16* dst = h == 0 ? p.dv : p.dk;
+      if constexpr (WIN) {
+        const ViewStrides& st = h == 0 ? p.dv_strides : p.dk_strides;
+        const int hkv = p.w.H / p.w.G, b = cur.bh / hkv;
+        dst += b * st.b + (cur.bh - b * hkv) * st.h + (row_ok ? key : 0) * st.n;
+      } else {
+        dst += (static_cast<size_t>(cur.bh) * p.N + (row_ok ? key : 0)) * L::D;
+      }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t r0[32], r1[32];

@@ -57,6 +57,7 @@
 #pragma once
 
 #include "fa_ptx.cuh"
+#include "fa_window.cuh"
 
 namespace fa {
 
@@ -78,6 +79,14 @@ struct FwdParams {
   int causal, mode;
   float beta, scale;
 };
+
+// The windowed forms of the forward kernels (WIN) take the same parameters and
+// the window.
+struct FwdWinParams : FwdParams {
+  WindowShape w;
+};
+template <bool WIN>
+using FwdArgs = std::conditional_t<WIN, FwdWinParams, FwdParams>;
 
 template <int D, bool HP = false>
 struct FwdLayout {
@@ -135,15 +144,25 @@ static_assert(FwdLayout<128, false>::o_col(1) + 128 <= 512 && FwdLayout<128, tru
 // tile; slot 1 may be empty (an odd number of Q tiles).  Causal: slot 0 is
 // query block n_qblk-1-2p and slot 1 the block below it, so slot 0 sees one
 // key tile more; without the mask both see all of them.
-template <int NT>
-struct FwdItem {
+// Windowed (WIN): slot 0 and slot 1 are neighbouring query blocks too, and the
+// item's key tiles are the union of what the two see, from slot 0's diagonal
+// tile downwards and then the sink tiles below the window; a slot skips the
+// tiles it does not see.  The diagonal tile comes first in each slot, so every
+// row has met a visible key before it meets a tile that hides all of its keys.
+struct FwdItemWindow {
+  // first window tile per slot, sink tiles of the launch, window tiles of the item, batch, heads
+  int lo[2], nsb, nwin, b, h, hk;
+};
+struct FwdItemPlain {};
+template <int NT, bool WIN = false>
+struct FwdItem : std::conditional_t<WIN, FwdItemWindow, FwdItemPlain> {
   int bh, qblk[2], nkv[2];
   bool valid1;
   __device__ __forceinline__ int nkv_max() const { return nkv[0]; }
   __device__ __forceinline__ bool has(int t) const { return t == 0 || valid1; }
   __device__ __forceinline__ static int count(const FwdParams& p) { return ((p.n_qblk + NT - 1) / NT) * p.BH; }
   // the r-th item of this CTA; false past the end of the list
-  __device__ __forceinline__ bool load(const FwdParams& p, int r) {
+  __device__ __forceinline__ bool load(const FwdArgs<WIN>& p, int r) {
     const int G = gridDim.x, c = blockIdx.x;
     const int w = r * G + ((r & 1) ? (G - 1 - c) : c);
     if (w >= count(p)) return false;
@@ -152,18 +171,56 @@ struct FwdItem {
     qblk[0] = p.n_qblk - 1 - NT * pr;
     qblk[1] = qblk[0] - 1;
     valid1 = NT == 2 && qblk[1] >= 0;
+    if constexpr (WIN) {
+      this->b = bh / p.w.H;
+      this->h = bh - this->b * p.w.H;
+      this->hk = this->h / p.w.G;
+      this->nsb = p.w.n_sink_blk;
+      this->lo[0] = p.w.first_block(qblk[0]);
+      this->lo[1] = valid1 ? p.w.first_block(qblk[1]) : this->lo[0];
+      this->nwin = qblk[0] - this->lo[1] + 1;
+      nkv[0] = this->nwin + (this->nsb < this->lo[1] ? this->nsb : this->lo[1]);
+      return true;
+    }
     nkv[0] = p.causal ? qblk[0] + 1 : p.n_qblk;
     nkv[1] = valid1 ? (p.causal ? qblk[1] + 1 : p.n_qblk) : 0;
     return true;
   }
+  // key tile of the item's step j
+  __device__ __forceinline__ int kblk(int j) const {
+    if constexpr (WIN)
+      return j < this->nwin ? qblk[0] - j : j - this->nwin;
+    else
+      return j;
+  }
+  // whether slot t works on step j
+  __device__ __forceinline__ bool active(int t, int j) const {
+    if constexpr (WIN) {
+      const int kb = kblk(j);
+      return has(t) && j < nkv[0] && kb <= qblk[t] && (kb >= this->lo[t] || kb < this->nsb);
+    } else {
+      return has(t) && j < nkv[t];
+    }
+  }
+  // slot t's first step (WIN: its diagonal tile)
+  __device__ __forceinline__ int first(int t) const { return WIN ? t : 0; }
+  // whether j is slot t's last step (for an active one)
+  __device__ __forceinline__ bool last(int t, int j) const {
+    // WIN: a slot can skip one tile between its window and its sinks
+    if constexpr (WIN)
+      return !active(t, j + 1) && !active(t, j + 2);
+    else
+      return j + 1 >= nkv[t];
+  }
 };
 
-template <int D, bool HP>
+template <int D, bool HP, bool WIN = false>
 __global__ void __launch_bounds__(512, 1)
 fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-              const FwdParams p) {
+              const FwdArgs<WIN> p) {
   using L = FwdLayout<D, HP>;
+  using Item = FwdItem<L::NT, WIN>;
   constexpr int NT = L::NT, QBUF = L::QBUF, KVS = L::KVS;
   constexpr bool kRawCompare = (D == 64);  // scale is exactly 1/8
   extern __shared__ uint8_t smem_raw[];
@@ -253,17 +310,20 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       auto store_staged = [&](int m) -> bool {
         const int b = m % QBUF;
         if (!wait(bar(L::O_STAGED + b), (m / QBUF) & 1, 1)) return false;
-        FwdItem<NT> it;
+        Item it;
         it.load(p, m);
         for (int t = 0; t < NT; ++t) {
           if (!it.has(t)) continue;
           for (int hh = 0; hh < D / 64; ++hh)
-            tma_store_3d(&tm_o, q_tile(b, t) + hh * L::HALF, 64 * hh, it.qblk[t] * L::BM, it.bh);
+            if constexpr (WIN)
+              tma_store_4d(&tm_o, q_tile(b, t) + hh * L::HALF, 64 * hh, it.qblk[t] * L::BM, it.h, it.b);
+            else
+              tma_store_3d(&tm_o, q_tile(b, t) + hh * L::HALF, 64 * hh, it.qblk[t] * L::BM, it.bh);
         }
         bulk_commit();
         return true;
       };
-      FwdItem<NT> it;
+      Item it;
       int n = 0, gk = 0;
       bool ok = true;
       for (; ok && it.load(p, n); ++n) {
@@ -278,8 +338,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         for (int t = 0; t < NT; ++t) {
           if (!it.has(t)) continue;
           for (int hh = 0; hh < D / 64; ++hh)
-            tma_load_3d(q_tile(b, t) + hh * L::HALF, &tm_q, bar(L::Q_FULL + b), 64 * hh, it.qblk[t] * L::BM,
-                        it.bh);
+            if constexpr (WIN)
+              tma_load_4d(q_tile(b, t) + hh * L::HALF, &tm_q, bar(L::Q_FULL + b), 64 * hh, it.qblk[t] * L::BM, it.h,
+                          it.b);
+            else
+              tma_load_3d(q_tile(b, t) + hh * L::HALF, &tm_q, bar(L::Q_FULL + b), 64 * hh, it.qblk[t] * L::BM,
+                          it.bh);
         }
         q_issued = n + 1;
         for (int j = 0; j < it.nkv_max(); ++j) {
@@ -287,8 +351,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (u > 0 && !wait(bar(L::K_EMPTY + s), (u - 1) & 1, 2)) { ok = false; break; }
           mbar_expect_tx(bar(L::K_FULL + s), L::TILE);
           for (int hh = 0; hh < D / 64; ++hh)
-            tma_load_3d(base + L::K_OFF + s * L::TILE + hh * L::HALF, &tm_k, bar(L::K_FULL + s), 64 * hh,
-                        j * L::BN, it.bh);
+            if constexpr (WIN)
+              tma_load_4d(base + L::K_OFF + s * L::TILE + hh * L::HALF, &tm_k, bar(L::K_FULL + s), 64 * hh,
+                          it.kblk(j) * L::BN, it.hk, it.b);
+            else
+              tma_load_3d(base + L::K_OFF + s * L::TILE + hh * L::HALF, &tm_k, bar(L::K_FULL + s), 64 * hh,
+                          j * L::BN, it.bh);
           k_issued = g + 1;
           if (g == 0) {
             // cold start: let the first Q K^T's operands arrive before the
@@ -298,8 +366,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (u > 0 && !wait(bar(L::V_EMPTY + s), (u - 1) & 1, 3)) { ok = false; break; }
           mbar_expect_tx(bar(L::V_FULL + s), L::TILE);
           for (int hh = 0; hh < D / 64; ++hh)
-            tma_load_3d(base + L::V_OFF + s * L::TILE + hh * L::HALF, &tm_v, bar(L::V_FULL + s), 64 * hh,
-                        j * L::BN, it.bh);
+            if constexpr (WIN)
+              tma_load_4d(base + L::V_OFF + s * L::TILE + hh * L::HALF, &tm_v, bar(L::V_FULL + s), 64 * hh,
+                          it.kblk(j) * L::BN, it.hk, it.b);
+            else
+              tma_load_3d(base + L::V_OFF + s * L::TILE + hh * L::HALF, &tm_v, bar(L::V_FULL + s), 64 * hh,
+                          j * L::BN, it.bh);
           v_issued = g + 1;
         }
         gk += it.nkv_max();
@@ -356,7 +428,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           }
         }
       };
-      FwdItem<NT> it;
+      Item it;
       int n = 0, gk = 0;
       int gs[2] = {0, 0}, ga[2] = {0, 0}, gi[2] = {0, 0};  // per slot: S steps, rescale steps, items
       bool ok = true;
@@ -369,7 +441,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (!wait(bar(L::K_FULL + s0), (gk / KVS) & 1, 5)) break;
           tc_fence_after();
           for (int t = 0; t < NT; ++t)
-            if (it.has(t)) issue_s(b, t, s0);
+            if (it.active(t, 0)) issue_s(b, t, s0);
           tc_commit(bar(L::K_EMPTY + s0));
           FA_TRACE_POINT(10);
         }
@@ -380,9 +452,13 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (!wait(bar(L::V_FULL + sv), (g / KVS) & 1, 8)) { ok = false; break; }
           if (next && !wait(bar(L::K_FULL + sk), ((g + 1) / KVS) & 1, 5)) { ok = false; break; }
           for (int t = 0; t < NT; ++t) {
-            if (!it.has(t) || j >= it.nkv[t]) continue;
+            if (!it.active(t, j)) {
+              // (WIN) a slot that skips this step may work on the next one
+              if (WIN && next && it.active(t, j + 1)) issue_s(b, t, sk);
+              continue;
+            }
             if (!wait(bar(L::P_FULL + t), gs[t] & 1, 7)) { ok = false; break; }
-            if (j == 0) {
+            if (j == it.first(t)) {
               // the first product of an item overwrites O_t: the previous
               // item's epilogue must have read it
               if (gi[t] > 0 && !wait(bar(L::O_FREE + t), (gi[t] - 1) & 1, 6)) { ok = false; break; }
@@ -391,11 +467,11 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               ++ga[t];
             }
             tc_fence_after();
-            issue_pv(t, sv, j > 0);
+            issue_pv(t, sv, j > it.first(t));
             ++gs[t];
-            if (j + 1 < it.nkv[t]) {
+            if (it.active(t, j + 1)) {
               issue_s(b, t, sk);  // after the product that reads P_bar_t from the same columns
-            } else {
+            } else if (it.last(t, j)) {
               tc_commit(bar(L::O_DONE + t));
               ++gi[t];
             }
@@ -419,7 +495,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     warpgroup_reg_dealloc<L::REGS_CORR>();
     const int r = threadIdx.x & 127;  // row within a tile == TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    FwdItem<NT> it;
+    Item it;
     int n = 0;
     int ga[2] = {0, 0}, gi[2] = {0, 0};
     bool ok = true;
@@ -429,7 +505,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       // the MMA warp issues the P_bar V products
       for (int j = 1; ok && j < it.nkv_max(); ++j) {
         for (int t = 0; t < NT; ++t) {
-          if (!it.has(t) || j >= it.nkv[t]) continue;
+          if (!it.active(t, j) || j == it.first(t)) continue;
           const int slot = ga[t] & 1;
           ok = wait.warp(bar(L::ALPHA_READY + 2 * slot + t), (ga[t] >> 1) & 1, 15);
           if (!ok) break;
@@ -534,17 +610,18 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const uint64_t EXPC2 = f2_pack(exp_c, exp_c);
     const float beta = p.beta;
     const bool stall = t == 0 && inject_stall_here(1u);  // test hook (fa_debug_inject_stall)
-    FwdItem<NT> it;
+    Item it;
     int n = 0, gs = 0, gi = 0, na = 0;
     bool ok = true;
     for (; ok && (NT == 2 || t == 0) && it.load(p, n); ++n) {
       if (!it.has(t)) continue;
-      const int qblk = it.qblk[t], nkv = it.nkv[t];
+      const int qblk = it.qblk[t], nkv = WIN ? it.nkv[0] : it.nkv[t];
       float rm_x = -INFINITY;    // running row max, x domain
       float m_run = -INFINITY;   // shift in force, S domain
       float l = 0.f;             // running sum of P_bar
       int rs = 0;
-      for (int j = 0; j < nkv; ++j, ++gs) {
+      for (int j = it.first(t); j < nkv; ++j) {
+        if (WIN && !it.active(t, j)) continue;
         ok = wait.warp(bar(L::S_FULL + t), gs & 1, 10);
         if (!ok) break;
         if (r == 0) FA_TRACE_POINT(20 + t);
@@ -557,7 +634,21 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(raw[c]);
         }
         // mask (diagonal tile / ragged tail); x[c] is key j*128 + c
-        {
+        if constexpr (WIN) {
+          const RowMask mk = p.w.row_mask(qblk * L::BM + r, it.kblk(j) * L::BN, p.N);
+          if (mk.hides(L::BN)) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t vis = mk.word(32 * w);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                x[32 * w + c] = (vis >> c) & 1u ? x[32 * w + c] * cmp_scale : -INFINITY;
+            }
+          } else if (!kRawCompare) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) x[c] *= cmp_scale;
+          }
+        } else {
           const int kv0 = j * L::BN;
           const bool diag = p.causal && (j == qblk);
           const int lim_causal = diag ? r : (L::BN - 1);
@@ -609,7 +700,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           m_new = (rm_s > 0.f) ? __fmul_rn(beta, rm_s) : ((rm_s < 0.f) ? 0.f : __fsub_rn(beta, 1.f));
           if (p.mode == 2 && __fsub_rn(m_new, rm_s) < kShiftMargin) m_new = __fadd_rn(rm_s, kShiftMargin);
         }
-        if (j > 0) {
+        if (j > it.first(t)) {
           // hand the rescale factor of O to the correction warps (1 if the
           // shift did not move); they rescale O_t while the exponentials run
           float alpha = 1.f;
@@ -670,6 +761,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         tmem_st_wait();
         tc_fence_before();
         if (!(stall && gs == 0)) mbar_arrive(bar(L::P_FULL + t));
+        ++gs;
         if (r == 0) FA_TRACE_POINT(24 + t);
       }
       if (!ok) break;

@@ -83,14 +83,20 @@ static_assert(2 * FwdSplitLayout<64, false>::SMEM_BYTES <= 228 * 1024, "two CTAs
 // The work items of one CTA, in order (see the file comment).  Only the
 // item's coordinates are held; the rest is read from the launch (kernel
 // parameters and the grid shape) when needed.
+// Windowed (WIN): an item's key tiles run from the diagonal tile down to the
+// window's first one, then over the sink tiles below it.  The diagonal tile
+// comes first, so every row has met a visible key before it meets a tile that
+// hides all of its keys.
+template <bool WIN>
 struct FwdSplitCursor {
   int r, qblk, bh, nkv;
   bool valid;
+  int nwin;  // WIN: window tiles of the item
   __device__ __forceinline__ static int item(int r) {
     const int G = gridDim.x, c = blockIdx.x;
     return r * G + ((r & 1) ? (G - 1 - c) : c);
   }
-  __device__ __forceinline__ void load(const FwdParams& p) {
+  __device__ __forceinline__ void load(const FwdArgs<WIN>& p) {
     const int w = item(r);
     valid = w < p.n_qblk * p.BH;
     if (valid) {
@@ -98,26 +104,39 @@ struct FwdSplitCursor {
       bh = w - tile_rev * p.BH;
       qblk = p.causal ? (p.n_qblk - 1 - tile_rev) : tile_rev;
       nkv = p.causal ? (qblk + 1) : p.n_qblk;
+      if constexpr (WIN) {
+        const int lo = p.w.first_block(qblk);
+        nwin = qblk - lo + 1;
+        nkv = nwin + (p.w.n_sink_blk < lo ? p.w.n_sink_blk : lo);
+      }
     }
   }
-  __device__ __forceinline__ void start(const FwdParams& p) {
+  // key tile of the item's step j
+  __device__ __forceinline__ int kblk(int j) const {
+    if constexpr (WIN)
+      return j < nwin ? qblk - j : j - nwin;
+    else
+      return j;
+  }
+  __device__ __forceinline__ void start(const FwdArgs<WIN>& p) {
     r = 0;
     load(p);
   }
-  __device__ __forceinline__ void next(const FwdParams& p) {
+  __device__ __forceinline__ void next(const FwdArgs<WIN>& p) {
     ++r;
     load(p);
   }
   // whether this CTA has a work item after the current one
-  __device__ __forceinline__ bool has_next(const FwdParams& p) const { return item(r + 1) < p.n_qblk * p.BH; }
+  __device__ __forceinline__ bool has_next(const FwdArgs<WIN>& p) const { return item(r + 1) < p.n_qblk * p.BH; }
 };
 
-template <int D, bool HP>
+template <int D, bool HP, bool WIN = false>
 __global__ void __launch_bounds__(384, FwdSplitLayout<D, HP>::CTAS_PER_SM)
 fa_fwd_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-              const FwdParams p) {
+              const FwdArgs<WIN> p) {
   using L = FwdSplitLayout<D, HP>;
+  using Cursor = FwdSplitCursor<WIN>;
   constexpr bool kRawCompare = (D == 64);  // scale is exactly 1/8
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -193,7 +212,7 @@ fa_fwd_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
       tma_prefetch_desc(&tm_o);
-      FwdSplitCursor cur;
+      Cursor cur;
       cur.start(p);
       // counts of the tiles issued so far, for the drain at exit
       int q_issued = 0, k_issued = 0, v_issued = 0;
@@ -201,11 +220,17 @@ fa_fwd_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       auto store_staged = [&](int m) -> bool {
         const int qs = m & 1;
         if (!wait(bar(L::O_STAGED + qs), (m >> 1) & 1, 1)) return false;
-        FwdSplitCursor it;
+        Cursor it;
         it.r = m;
         it.load(p);
         for (int hh = 0; hh < D / 64; ++hh)
-          tma_store_3d(&tm_o, base + L::Q_OFF + qs * L::TILE + hh * L::HALF, 64 * hh, it.qblk * L::BM, it.bh);
+          if constexpr (WIN) {
+            const int b = it.bh / p.w.H;
+            tma_store_4d(&tm_o, base + L::Q_OFF + qs * L::TILE + hh * L::HALF, 64 * hh, it.qblk * L::BM,
+                         it.bh - b * p.w.H, b);
+          } else {
+            tma_store_3d(&tm_o, base + L::Q_OFF + qs * L::TILE + hh * L::HALF, 64 * hh, it.qblk * L::BM, it.bh);
+          }
         bulk_commit();
         return true;
       };
@@ -215,7 +240,7 @@ fa_fwd_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
       // then waits only for the Q K^T two tiles back; loading V(j) before
       // K(j+1) tied each K load to the P V product two tiles back, and the
       // softmax warps waited ~600 cycles per tile for their next S.
-      auto load_q = [&](const FwdSplitCursor& c, int m) -> bool {
+      auto load_q = [&](const Cursor& c, int m) -> bool {
         const int qs = m & 1;
         if (m >= 2) {
           // item m-2's O is staged in this buffer: store it, and reuse the
@@ -225,28 +250,46 @@ fa_fwd_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         mbar_expect_tx(bar(L::Q_FULL + qs), L::TILE);
         for (int hh = 0; hh < D / 64; ++hh)
-          tma_load_3d(base + L::Q_OFF + qs * L::TILE + hh * L::HALF, &tm_q, bar(L::Q_FULL + qs), 64 * hh,
-                      c.qblk * L::BM, c.bh);
+          if constexpr (WIN) {
+            const int b = c.bh / p.w.H;
+            tma_load_4d(base + L::Q_OFF + qs * L::TILE + hh * L::HALF, &tm_q, bar(L::Q_FULL + qs), 64 * hh,
+                        c.qblk * L::BM, c.bh - b * p.w.H, b);
+          } else {
+            tma_load_3d(base + L::Q_OFF + qs * L::TILE + hh * L::HALF, &tm_q, bar(L::Q_FULL + qs), 64 * hh,
+                        c.qblk * L::BM, c.bh);
+          }
         q_issued = m + 1;
         return true;
       };
-      auto load_k = [&](const FwdSplitCursor& c, int j, int g) -> bool {
+      auto load_k = [&](const Cursor& c, int j, int g) -> bool {
         const int s = g & 1, u = g >> 1;
         if (u > 0 && !wait(bar(L::K_EMPTY + s), (u - 1) & 1, 2)) return false;
         mbar_expect_tx(bar(L::K_FULL + s), L::TILE);
         for (int hh = 0; hh < D / 64; ++hh)
-          tma_load_3d(base + L::K_OFF + s * L::TILE + hh * L::HALF, &tm_k, bar(L::K_FULL + s), 64 * hh,
-                      j * L::BN, c.bh);
+          if constexpr (WIN) {
+            const int b = c.bh / p.w.H;
+            tma_load_4d(base + L::K_OFF + s * L::TILE + hh * L::HALF, &tm_k, bar(L::K_FULL + s), 64 * hh,
+                        c.kblk(j) * L::BN, (c.bh - b * p.w.H) / p.w.G, b);
+          } else {
+            tma_load_3d(base + L::K_OFF + s * L::TILE + hh * L::HALF, &tm_k, bar(L::K_FULL + s), 64 * hh,
+                        j * L::BN, c.bh);
+          }
         k_issued = g + 1;
         return true;
       };
-      auto load_v = [&](const FwdSplitCursor& c, int j, int g) -> bool {
+      auto load_v = [&](const Cursor& c, int j, int g) -> bool {
         const int s = g & 1, u = g >> 1;
         if (u > 0 && !wait(bar(L::V_EMPTY + s), (u - 1) & 1, 3)) return false;
         mbar_expect_tx(bar(L::V_FULL + s), L::TILE);
         for (int hh = 0; hh < D / 64; ++hh)
-          tma_load_3d(base + L::V_OFF + s * L::TILE + hh * L::HALF, &tm_v, bar(L::V_FULL + s), 64 * hh,
-                      j * L::BN, c.bh);
+          if constexpr (WIN) {
+            const int b = c.bh / p.w.H;
+            tma_load_4d(base + L::V_OFF + s * L::TILE + hh * L::HALF, &tm_v, bar(L::V_FULL + s), 64 * hh,
+                        c.kblk(j) * L::BN, (c.bh - b * p.w.H) / p.w.G, b);
+          } else {
+            tma_load_3d(base + L::V_OFF + s * L::TILE + hh * L::HALF, &tm_v, bar(L::V_FULL + s), 64 * hh,
+                        j * L::BN, c.bh);
+          }
         v_issued = g + 1;
         return true;
       };
@@ -262,7 +305,7 @@ fa_fwd_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           if (j + 1 < cur.nkv) {
             ok = load_k(cur, j + 1, gt + 1);
           } else if (cur.has_next(p)) {
-            FwdSplitCursor nx = cur;
+            Cursor nx = cur;
             nx.next(p);
             ok = load_k(nx, 0, gt + 1) && load_q(nx, n + 1);
           }
@@ -315,7 +358,7 @@ fa_fwd_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         tc_commit(bar(L::S_FULL));
         tc_commit(bar(L::K_EMPTY + s));
       };
-      FwdSplitCursor cur;
+      Cursor cur;
       cur.start(p);
       int n = 0, gt = 0;
       bool ok = cur.valid && wait(bar(L::Q_FULL), 0, 4) && wait(bar(L::K_FULL), 0, 5);
@@ -386,7 +429,7 @@ fa_fwd_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     // reaches.
     bool ok = true;
     const bool stall = inject_stall_here(1u);  // test hook (fa_debug_inject_stall)
-    FwdSplitCursor cur;
+    Cursor cur;
     cur.start(p);
     int gt = 0;
     for (; cur.valid; cur.next(p)) {
@@ -416,17 +459,33 @@ fa_fwd_split_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
           mbar_arrive(bar(L::S_FREE));
           if (threadIdx.x == 0) FA_TRACE_POINT(21);
           // mask (diagonal tile / ragged tail); column index of x[c] is 64h + c
-          const int kv0 = j * L::BN;
-          const bool diag = p.causal && (j == qblk);
-          const int lim_causal = diag ? t : (L::BN - 1);
-          const int lim_len = p.N - 1 - kv0;
-          const int lim = (lim_causal < lim_len ? lim_causal : lim_len) - 64 * h;  // last visible local column
-          if (lim < 63) {
+          if constexpr (WIN) {
+            const RowMask mk = p.w.row_mask(qblk * L::BM + t, cur.kblk(j) * L::BN + 64 * h, p.N);
+            if (mk.hides(64)) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = (c <= lim) ? x[c] * cmp_scale : -INFINITY;
-          } else if (!kRawCompare) {
+              for (int w = 0; w < 2; ++w) {
+                const uint32_t vis = mk.word(32 * w);
 #pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] *= cmp_scale;
+                for (int c = 0; c < 32; ++c)
+                  x[32 * w + c] = (vis >> c) & 1u ? x[32 * w + c] * cmp_scale : -INFINITY;
+              }
+            } else if (!kRawCompare) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c) x[c] *= cmp_scale;
+            }
+          } else {
+            const int kv0 = j * L::BN;
+            const bool diag = p.causal && (j == qblk);
+            const int lim_causal = diag ? t : (L::BN - 1);
+            const int lim_len = p.N - 1 - kv0;
+            const int lim = (lim_causal < lim_len ? lim_causal : lim_len) - 64 * h;  // last visible local column
+            if (lim < 63) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c) x[c] = (c <= lim) ? x[c] * cmp_scale : -INFINITY;
+            } else if (!kRawCompare) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c) x[c] *= cmp_scale;
+            }
           }
           // this half's maximum (three-input max, eight partial maxima)
           float pm[8];

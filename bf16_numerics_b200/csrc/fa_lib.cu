@@ -17,6 +17,7 @@
 #include "fa_bwd_pipe.cuh"
 #include "fa_bwd_pipe128.cuh"
 #include "fa_fwd_split.cuh"
+#include "fa_window_bwd.cuh"
 
 namespace {
 
@@ -309,9 +310,9 @@ fa_status launch_bwd(const void* q, const void* k, const void* v, const void* o,
   using LP128 = fa::BwdPipe128Layout;
   static std::atomic<uint64_t> attr{0};
   if (D == 64) {
-    if (!ensure_smem(fa::fa_bwd_main_pipe_kernel, LP::SMEM_BYTES, attr)) return FA_ERR_CUDA;
+    if (!ensure_smem(fa::fa_bwd_main_pipe_kernel<false>, LP::SMEM_BYTES, attr)) return FA_ERR_CUDA;
   } else {
-    if (!ensure_smem(fa::fa_bwd_main_pipe128_kernel, LP128::SMEM_BYTES, attr)) return FA_ERR_CUDA;
+    if (!ensure_smem(fa::fa_bwd_main_pipe128_kernel<false>, LP128::SMEM_BYTES, attr)) return FA_ERR_CUDA;
   }
   const long long rows = static_cast<long long>(BH) * N;
   const int n_blk = (N + 127) / 128;
@@ -378,14 +379,14 @@ fa_status launch_bwd(const void* q, const void* k, const void* v, const void* o,
       if (!make_map(&mdk, dk, BH, N, D) || !make_map(&mdv, dv, BH, N, D))
         return cuda_fail("cuTensorMapEncodeTiled (dk/dv)");
       LaunchTimer tm(FA_KERNEL_BWD_MAIN, stream);
-      cudaError_t e = launch_pdl(fa::fa_bwd_main_pipe_kernel, dim3(pgrid), dim3(LP::THREADS), LP::SMEM_BYTES, stream,
+      cudaError_t e = launch_pdl(fa::fa_bwd_main_pipe_kernel<false>, dim3(pgrid), dim3(LP::THREADS), LP::SMEM_BYTES, stream,
                                  mq, mk, mv, mdo, mdq, mdk, mdv, p);
       tm.done();
       if (e == cudaSuccess) e = cudaGetLastError();
       if (e != cudaSuccess) return cuda_fail("fa_bwd main kernel launch", e);
     } else {
       LaunchTimer tm(FA_KERNEL_BWD_MAIN, stream);
-      cudaError_t e = launch_pdl(fa::fa_bwd_main_pipe128_kernel, dim3(pgrid), dim3(LP128::THREADS),
+      cudaError_t e = launch_pdl(fa::fa_bwd_main_pipe128_kernel<false>, dim3(pgrid), dim3(LP128::THREADS),
                                  LP128::SMEM_BYTES, stream, mq, mk, mv, mdo, mdq, p);
       tm.done();
       if (e == cudaSuccess) e = cudaGetLastError();
@@ -642,3 +643,5 @@ extern "C" fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v,
   return fa_bwd(q, k, v, o, dO, lse, row_m, dq, dk, dv, scratch, FA_NOALLOC_SCRATCH_BYTES, B, H, N, d, causal,
                 softmax_mode, beta, stream);
 }
+
+#include "fa_window_host.cuh"

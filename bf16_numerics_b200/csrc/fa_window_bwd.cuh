@@ -1,0 +1,113 @@
+// Delta preprocess and dQ convert of the windowed backward, for arrays given
+// by strides (the main kernels are the WIN forms of fa_bwd_pipe.cuh and
+// fa_bwd_pipe128.cuh).  Both are bound by memory traffic, like the contiguous
+// forms in fa_bwd.cuh; the differences are the addressing (work comes in
+// groups of rows of one head, so that the two divisions of a group's index are
+// shared by its rows) and what the clear covers.
+#pragma once
+
+#include "fa_bwd.cuh"
+
+namespace fa {
+
+// delta[(b*H + h)*N + n] = sum_c dO * O in fp32.  The first clear_blocks blocks
+// zero `clear4` float4 starting at `clear` (the dQ accumulator and what
+// follows it) before they wait for the grid ahead: see fa_bwd_delta_kernel for
+// how the host picks their number and why dependents launch only after the
+// wait.
+template <int D>
+__global__ void __launch_bounds__(128, 16)
+fa_window_delta_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dO, ViewStrides so,
+                       ViewStrides sdo, float* __restrict__ delta, float4* __restrict__ clear, long long clear4, int H,
+                       int N, long long groups, int groups_per_head, int clear_blocks) {
+  constexpr int LPR = D / 8;     // lanes per row (8 elements per lane)
+  constexpr int RPW = 32 / LPR;  // rows per warp per pass
+  constexpr int U = 2;           // passes per group: RPW * U rows, all loads before any use
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / LPR, li = lane % LPR;
+  if (static_cast<int>(blockIdx.x) < clear_blocks) {
+    const long long lo = clear4 * blockIdx.x / clear_blocks, hi = clear4 * (blockIdx.x + 1) / clear_blocks;
+    for (long long i = lo + threadIdx.x; i < hi; i += blockDim.x) clear[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  grid_dependency_wait();  // O comes from the forward grid
+  grid_launch_dependents();
+  const long long warp_global = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const long long n_warps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+  for (long long g = warp_global; g < groups; g += n_warps) {
+    const long long bh = g / groups_per_head;
+    const int n0 = static_cast<int>(g - bh * groups_per_head) * (RPW * U);
+    const long long b = bh / H;
+    const int h = static_cast<int>(bh - b * H);
+    const __nv_bfloat16* po = o + b * so.b + h * so.h + 8 * li;
+    const __nv_bfloat16* pd = dO + b * sdo.b + h * sdo.h + 8 * li;
+    ORaw<__nv_bfloat16> a[U];
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long n = n0 + u * RPW + sub;
+      if (n < N) {
+        a[u].load(po + n * so.n);
+        v[u] = __ldg(reinterpret_cast<const uint4*>(pd + n * sdo.n));
+      } else {
+        a[u].zero();
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float acc = a[u].dot(v[u], 0.f);
+#pragma unroll
+      for (int off = LPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+      const long long n = n0 + u * RPW + sub;
+      if (n < N && li == 0) delta[bh * N + n] = acc;
+    }
+  }
+}
+
+// dq = bf16(dq_acc): tiles of 8192 elements of one head (256 threads, four
+// chunks of 8 elements each, loads first).
+template <int D>
+__global__ void __launch_bounds__(256)
+fa_window_dq_convert_kernel(const float* __restrict__ dq_acc, __nv_bfloat16* __restrict__ dq, ViewStrides sdq, int H,
+                            int N, long long tiles, int tiles_per_head) {
+  constexpr int U = 4, CPR = D / 8;         // chunks per row
+  constexpr int ROWS = 256 * U / CPR;       // rows per tile
+  grid_dependency_wait();  // the accumulator is complete once the main grid is
+  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const long long bh = tile / tiles_per_head;
+    const int n0 = static_cast<int>(tile - bh * tiles_per_head) * ROWS;
+    const long long b = bh / H;
+    const int h = static_cast<int>(bh - b * H);
+    const float4* src = reinterpret_cast<const float4*>(dq_acc + bh * N * D);
+    __nv_bfloat16* dst = dq + b * sdq.b + h * sdq.h;
+    float4 x[U], y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = threadIdx.x + 256 * u;
+      const long long n = n0 + i / CPR;
+      if (n < N) {
+        x[u] = __ldcs(src + n * (D / 4) + 2 * (i % CPR));
+        y[u] = __ldcs(src + n * (D / 4) + 2 * (i % CPR) + 1);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = threadIdx.x + 256 * u;
+      const long long n = n0 + i / CPR;
+      if (n < N) {
+        uint4 w;
+        w.x = pack_bf16x2(x[u].x, x[u].y);
+        w.y = pack_bf16x2(x[u].z, x[u].w);
+        w.z = pack_bf16x2(y[u].x, y[u].y);
+        w.w = pack_bf16x2(y[u].z, y[u].w);
+        *reinterpret_cast<uint4*>(dst + n * sdq.n + 8 * (i % CPR)) = w;
+      }
+    }
+  }
+  // a later call's delta kernel clears the accumulator before its own
+  // dependency wait: let it start only once every read here has been used
+  __syncthreads();
+  grid_launch_dependents();
+}
+
+}  // namespace fa

@@ -143,6 +143,50 @@ fa_status fa_bwd_o_hp(const void* q, const void* k, const void* v, const float* 
                       size_t workspace_bytes, int B, int H, int N, int d, int causal, int softmax_mode, float beta,
                       void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Sliding window with sinks, shared heads, strided arrays.
+ *
+ * fa_window_fwd / fa_window_bwd compute the attention above with the mask
+ *
+ *   key j is visible to query i  <=>  j <= i and (i - j < window or j < sinks)
+ *
+ * -- causal, the last `window` keys of each row (its own included), and the
+ * first `sinks` keys of the sequence -- with the same shift rule, row
+ * statistics, lse and backward formulas.  window >= 1; a window of N or more
+ * is plain causal attention.  sinks >= 0.
+ *
+ * Shared heads: q, o, dO, dq have H heads, k, v, dk, dv have Hkv, H a multiple
+ * of Hkv; query head h reads key head h / (H / Hkv), and dK, dV of a key head
+ * are the sums over the query heads that read it.
+ *
+ * fa_view: a bf16 array [B, H, N, d] (or [B, Hkv, N, d]) whose element
+ * (b, h, n, c) is at ptr[b*stride_b + h*stride_h + n*stride_n + c].  ptr is
+ * 16-byte aligned; along every axis of more than one entry the stride is a
+ * positive multiple of 8 elements below 2^39, and no two elements share
+ * memory (so no stride-0 broadcasting).  [B, N, H, d] storage and slices of a
+ * fused projection are such views.  lse, row_m and the row statistics are
+ * contiguous [B, H, N].
+ *
+ * Workspace, stream and errors are those of fa_fwd / fa_bwd.  dK and dV of a
+ * call are reproducible unless the workspace query says otherwise below; dQ
+ * sums fp32 partials in an order that varies (as in fa_bwd). */
+typedef struct {
+  void* ptr;
+  long long stride_b, stride_h, stride_n;
+} fa_view;
+
+fa_status fa_window_fwd(const fa_view* q, const fa_view* k, const fa_view* v, const fa_view* o, float* lse,
+                        const fa_row_stats* stats, int B, int H, int Hkv, int N, int d, int window, int sinks,
+                        int softmax_mode, float beta, void* stream);
+
+/* Bytes of workspace fa_window_bwd needs; 0 on bad sizes. */
+size_t fa_window_bwd_workspace_bytes(int B, int H, int Hkv, int N, int d, int window, int sinks);
+
+fa_status fa_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v, const fa_view* o, const fa_view* dO,
+                        const float* lse, const float* row_m, const fa_view* dq, const fa_view* dk, const fa_view* dv,
+                        void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int N, int d, int window,
+                        int sinks, int softmax_mode, float beta, void* stream);
+
 /* Static description of a status code. */
 const char* fa_status_string(fa_status s);
 
