@@ -30,7 +30,8 @@ __all__ = ["FaError", "STANDARD", "STABILIZED", "STABILIZED_MARGIN", "RowStats",
            "fa_bwd_workspace_offsets", "fa_status_string", "fa_device_error", "fa_timing_enable",
            "fa_timing_read", "fa_debug_set_wait_limit_ns", "fa_debug_inject_stall", "attention_forward",
            "attention_backward", "library_path", "NO_WINDOW", "fa_window_fwd", "fa_window_bwd",
-           "fa_window_bwd_workspace_bytes", "window_attention_forward", "window_attention_backward"]
+           "fa_window_bwd_workspace_bytes", "window_attention_forward", "window_attention_backward",
+           "fa_cached_workspace_bytes", "fa_cached_fwd", "fa_cache_append", "fa_cache_compact", "cached_attention"]
 
 
 class FaError(RuntimeError):
@@ -373,3 +374,86 @@ def window_attention_backward(q, k, v, o, dO, lse, row_m, window: int = NO_WINDO
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_window_bwd(q, k, v, o, dO, lse, row_m, dq, dk, dv, workspace, window, sinks, softmax_mode, beta, stream)
     return dq, dk, dv, workspace
+
+
+# ------------------------------------------------------------- a paged cache
+
+def _pool(k_pages, v_pages, page_table, ctx_len, device):
+    """(pointers, (num_pages, page_size, table_width), B, Hkv, d) of a cache."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be a bfloat16 tensor [num_pages, Hkv, page_size, d]")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 tensor [B, table_width]")
+    P, Hkv, page, d = k_pages.shape
+    B, width = page_table.shape
+    ptrs = (_vec("k_pages", k_pages, (P, Hkv, page, d), device, torch.bfloat16),
+            _vec("v_pages", v_pages, (P, Hkv, page, d), device, torch.bfloat16),
+            _vec("page_table", page_table, (B, width), device, torch.int32),
+            _vec("ctx_len", ctx_len, (B,), device, torch.int32))
+    return ptrs, (P, page, width), B, Hkv, d
+
+
+def fa_cached_workspace_bytes(B: int, H: int, Hkv: int, T: int, d: int) -> int:
+    return int(_abi.load().fa_cached_workspace_bytes(B, H, Hkv, T, d))
+
+
+def fa_cached_fwd(q, k_pages, v_pages, page_table, ctx_len, tree, o, lse, workspace, window: int = NO_WINDOW,
+                  sinks: int = 0, softmax_mode: int = STABILIZED, beta: float = 2.0, stream=None) -> None:
+    """C ``fa_cached_fwd``: attention of the T new tokens of q [B, H, T, d] over a paged cache that holds them already.
+
+    tree: None (each new token sees itself and those before it) or int64 [B, T], the bits of word t naming the new
+    tokens that token t sees.  page_table int32 [B, table_width], ctx_len int32 [B], workspace uint8."""
+    device = _device_of(q)
+    B, H, T, d = q.shape
+    ptrs, sizes, tB, Hkv, td = _pool(k_pages, v_pages, page_table, ctx_len, device)
+    if tB != B or td != d:
+        raise ValueError(f"q is [{B}, {H}, {T}, {d}], the page table has {tB} rows and the pages rows of {td}")
+    code = _call(device, stream, _abi.load().fa_cached_fwd, _view("q", q, q.shape, device), *ptrs,
+                 None if tree is None else _vec("tree", tree, (B, T), device, torch.int64),
+                 _view("o", o, q.shape, device), _vec("lse", lse, (B, H, T), device),
+                 _vec("workspace", workspace, (workspace.numel(),), device, torch.uint8), workspace.numel(),
+                 B, H, Hkv, T, d, *sizes, window, sinks, softmax_mode, beta)
+    if code != _abi.FA_OK:
+        raise FaError(code, "fa_cached_fwd")
+
+
+def cached_attention(q, k_pages, v_pages, page_table, ctx_len, tree=None, window: int = NO_WINDOW, sinks: int = 0,
+                     softmax_mode: int = STABILIZED, beta: float = 2.0, workspace=None, stream=None):
+    """Allocate outputs (torch; o strided like q), and a workspace if none is given, and run fa_cached_fwd.
+    Returns (o, lse)."""
+    device = _device_of(q)
+    B, H, T, d = q.shape
+    with _allocate_on(stream):
+        if workspace is None:
+            workspace = torch.empty(fa_cached_workspace_bytes(B, H, k_pages.shape[1], T, d), device=device,
+                                    dtype=torch.uint8)
+        o = torch.empty_like(q)
+        lse = torch.empty(B, H, T, device=device, dtype=torch.float32)
+    fa_cached_fwd(q, k_pages, v_pages, page_table, ctx_len, tree, o, lse, workspace, window, sinks, softmax_mode,
+                  beta, stream)
+    return o, lse
+
+
+def fa_cache_append(k, v, k_pages, v_pages, page_table, ctx_len, count=None, stream=None) -> None:
+    """C ``fa_cache_append``: row t of k, v [B, Hkv, T, d] into slot ctx_len[b] + t, for t < count[b] (None: all)."""
+    device = _device_of(k)
+    B, Hkv, T, d = k.shape
+    ptrs, sizes, tB, pH, td = _pool(k_pages, v_pages, page_table, ctx_len, device)
+    if (tB, pH, td) != (B, Hkv, d):
+        raise ValueError(f"k is [{B}, {Hkv}, {T}, {d}], the cache has {tB} sequences, {pH} heads and rows of {td}")
+    code = _call(device, stream, _abi.load().fa_cache_append, _view("k", k, k.shape, device),
+                 _view("v", v, k.shape, device), *ptrs,
+                 None if count is None else _vec("count", count, (B,), device, torch.int32), B, Hkv, T, d, *sizes)
+    if code != _abi.FA_OK:
+        raise FaError(code, "fa_cache_append")
+
+
+def fa_cache_compact(k_pages, v_pages, page_table, ctx_len, src, count, stream=None) -> None:
+    """C ``fa_cache_compact``: slot ctx_len[b] + i takes the row of slot ctx_len[b] + src[b, i], for i < count[b]."""
+    device = _device_of(k_pages)
+    ptrs, sizes, B, Hkv, d = _pool(k_pages, v_pages, page_table, ctx_len, device)
+    M = src.shape[1] if isinstance(src, torch.Tensor) and src.dim() == 2 else -1
+    code = _call(device, stream, _abi.load().fa_cache_compact, *ptrs, _vec("src", src, (B, M), device, torch.int32),
+                 _vec("count", count, (B,), device, torch.int32), B, Hkv, M, d, *sizes)
+    if code != _abi.FA_OK:
+        raise FaError(code, "fa_cache_compact")

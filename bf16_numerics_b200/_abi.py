@@ -17,6 +17,7 @@ FA_ERR_UNSUPPORTED = 2
 FA_ERR_WORKSPACE = 3
 FA_ERR_CUDA = 4
 FA_ERR_TIMEOUT = 5
+FA_ERR_BAD_PAGE = 6
 
 FA_SOFTMAX_STANDARD = 0
 FA_SOFTMAX_STABILIZED = 1
@@ -32,6 +33,8 @@ FA_NUM_KERNELS = 4
 FA_ERRWORD_FWD = 1
 FA_ERRWORD_BWD_D64 = 3
 FA_ERRWORD_BWD_D128 = 4
+FA_ERRWORD_CACHED = 5
+FA_ERRWORD_CACHE_PAGE = 6
 KERNEL_NAMES = ("fa_fwd_kernel", "fa_bwd_delta_kernel", "fa_bwd_main_kernel", "fa_bwd_dq_convert_kernel")
 
 # every symbol include/fa_b200.h declares
@@ -39,7 +42,8 @@ EXPORTS = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_bwd_workspace_delta
            "fa_bwd_workspace_dq_offset", "fa_status_string", "fa_device_error", "fa_timing_enable",
            "fa_timing_read", "fa_bwd_noalloc", "fa_last_error_string", "fa_fwd_o_hp", "fa_bwd_o_hp",
            "fa_debug_set_wait_limit_ns", "fa_debug_inject_stall", "fa_window_fwd", "fa_window_bwd",
-           "fa_window_bwd_workspace_bytes")
+           "fa_window_bwd_workspace_bytes", "fa_cached_workspace_bytes", "fa_cached_fwd", "fa_cache_append",
+           "fa_cache_compact")
 
 
 class FaRowStats(ctypes.Structure):
@@ -81,6 +85,14 @@ def load() -> ctypes.CDLL:
     lib.fa_window_bwd.restype = i
     lib.fa_window_bwd_workspace_bytes.argtypes = [i] * 7
     lib.fa_window_bwd_workspace_bytes.restype = sz
+    lib.fa_cached_workspace_bytes.argtypes = [i] * 5
+    lib.fa_cached_workspace_bytes.restype = sz
+    lib.fa_cached_fwd.argtypes = [view] + [vp] * 5 + [view, vp, vp, sz] + [i] * 11 + [f, vp]
+    lib.fa_cached_fwd.restype = i
+    lib.fa_cache_append.argtypes = [view, view] + [vp] * 5 + [i] * 7 + [vp]
+    lib.fa_cache_append.restype = i
+    lib.fa_cache_compact.argtypes = [vp] * 6 + [i] * 7 + [vp]
+    lib.fa_cache_compact.restype = i
     lib.fa_status_string.argtypes = [i]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_last_error_string.argtypes = []

@@ -18,6 +18,7 @@
 #include "fa_bwd_pipe128.cuh"
 #include "fa_fwd_split.cuh"
 #include "fa_window_bwd.cuh"
+#include "fa_cache_ops.cuh"
 
 namespace {
 
@@ -417,6 +418,7 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case FA_ERR_CUDA: return "CUDA call or kernel launch failed";
     case FA_ERR_TIMEOUT: return "a kernel gave up on a bounded wait";
+    case FA_ERR_BAD_PAGE: return "a page id, length or index outside the cache";
   }
   return "unknown status";
 }
@@ -539,7 +541,7 @@ fa_status fa_device_error(unsigned int* code) {
   if (v != 0) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(fa::g_fa_error, &zero, sizeof(zero)) != cudaSuccess) return FA_ERR_CUDA;
-    return FA_ERR_TIMEOUT;
+    return (v >> 24) == FA_ERRWORD_CACHE_PAGE ? FA_ERR_BAD_PAGE : FA_ERR_TIMEOUT;
   }
   return FA_OK;
 }
@@ -645,3 +647,4 @@ extern "C" fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v,
 }
 
 #include "fa_window_host.cuh"
+#include "fa_cached_host.cuh"

@@ -74,7 +74,8 @@ typedef enum {
   FA_ERR_UNSUPPORTED = 2,  /* valid request outside the implemented domain (d, N) */
   FA_ERR_WORKSPACE = 3,    /* workspace missing, misaligned or too small */
   FA_ERR_CUDA = 4,         /* a CUDA runtime/driver call or kernel launch failed */
-  FA_ERR_TIMEOUT = 5       /* a kernel gave up on a bounded wait (see fa_device_error) */
+  FA_ERR_TIMEOUT = 5,      /* a kernel gave up on a bounded wait (see fa_device_error) */
+  FA_ERR_BAD_PAGE = 6      /* a kernel met a page id, length or index outside the cache (see fa_device_error) */
 } fa_status;
 
 typedef enum {
@@ -187,6 +188,69 @@ fa_status fa_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v, co
                         void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int N, int d, int window,
                         int sinks, int softmax_mode, float beta, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention over a paged key/value cache, and the cache's writes.
+ *
+ * The cache: k_pages and v_pages are bf16 pools [num_pages, Hkv, page_size, d],
+ * contiguous and 16-byte aligned, page_size one of 16, 32, 64, 128, 256.  Row b of
+ * page_table (int32 [B, table_width]) names the pages of sequence b in order:
+ * its slot j is row j % page_size of page page_table[b][j / page_size].
+ * ctx_len (int32 [B]) is the number of tokens sequence b holds; slot j <
+ * ctx_len[b] holds the token at position j.  Lengths, tables, trees and counts
+ * are read on the device when the kernels run, so a captured call follows
+ * them.  Entries of the table that a call has no need of may hold anything.
+ * table_width * page_size < 2^31.
+ *
+ * fa_cached_fwd: attention of T new tokens per sequence, 1 <= T <= 64, whose
+ * keys and values are already in slots ctx_len[b] .. ctx_len[b] + T - 1
+ * (fa_cache_append puts them there).  q and o are views [B, H, T, d], lse is
+ * contiguous fp32 [B, H, T], H a multiple of Hkv.  tree: uint64 [B, T], bit u of
+ * word t set when token t sees new token u (bits from T on are ignored; its own
+ * bit is normally set); NULL: a chain, every token sees itself and the new
+ * tokens before it.  Token t stands at position
+ * pos(t) = ctx_len[b] + popcount(word t) - 1 and sees
+ *   slot j < ctx_len[b]  if  pos(t) - j < window or j < sinks,
+ *   new token u          if  its bit is set and (pos(t) - pos(u) < window or pos(u) < sinks).
+ * A token whose word is zero is absent: o = 0 and lse = -inf in its row, and its
+ * slot need not have been written.  window >= 1 (2^31 - 1: no window), sinks
+ * >= 0.  Softmax modes as in fa_fwd; the context is processed in parts that are
+ * joined at the end, and the shift rule applies to the keys of each part.
+ * With tied maxima the rule moves the shift by |rm| (beta - 1) or |rm|: as in
+ * fa_fwd, rows with a tied maximum beyond about 80 in size underflow.
+ *
+ * Slots below ctx_len[b] of a page any slot of which is visible, and the slots
+ * of tokens that are not absent, hold finite values; anything may lie in other
+ * slots.  A length below zero or beyond the table (ctx_len[b] + T > table_width
+ * * page_size) makes the sequence's rows empty; a page id outside the pool is
+ * read as zeros; both are reported as FA_ERR_BAD_PAGE by fa_device_error.
+ *
+ * workspace: fa_cached_workspace_bytes of device memory, 256-byte aligned; its
+ * contents on entry do not matter.  Calls that may overlap on the GPU need one
+ * each.  Two kernels.  Results are reproducible on the same GPU model. */
+size_t fa_cached_workspace_bytes(int B, int H, int Hkv, int T, int d);
+fa_status fa_cached_fwd(const fa_view* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                        const int32_t* ctx_len, const uint64_t* tree, const fa_view* o, float* lse, void* workspace,
+                        size_t workspace_bytes, int B, int H, int Hkv, int T, int d, int num_pages, int page_size,
+                        int table_width, int window, int sinks, int softmax_mode, float beta, void* stream);
+
+/* Writes row t of k and v (views [B, Hkv, T, d]) into slot ctx_len[b] + t, for
+ * t < count[b] (int32 [B]; NULL: all T).  ctx_len is not changed.  Any T with T *
+ * Hkv * d < 2^34.  A slot or page outside the cache, or a count outside [0, T],
+ * writes nothing and is reported as FA_ERR_BAD_PAGE by fa_device_error.  No two
+ * sequences may write the same slot of a page. */
+fa_status fa_cache_append(const fa_view* k, const fa_view* v, void* k_pages, void* v_pages, const int32_t* page_table,
+                          const int32_t* ctx_len, const int32_t* count, int B, int Hkv, int T, int d, int num_pages,
+                          int page_size, int table_width, void* stream);
+
+/* Moves accepted drafted tokens up behind the context: slot ctx_len[b] + i
+ * takes the keys and values that slot ctx_len[b] + src[b][i] held before the
+ * call, for i < count[b] (src int32 [B, M], 1 <= M <= 64; count int32 [B], 0 <=
+ * count[b] <= M).  src[b][i] >= 0, in any order; a slot may be named twice.  Errors as
+ * in fa_cache_append; the pages that a call writes belong to one sequence. */
+fa_status fa_cache_compact(void* k_pages, void* v_pages, const int32_t* page_table, const int32_t* ctx_len,
+                           const int32_t* src, const int32_t* count, int B, int Hkv, int M, int d, int num_pages,
+                           int page_size, int table_width, void* stream);
+
 /* Static description of a status code. */
 const char* fa_status_string(fa_status s);
 
@@ -199,8 +263,19 @@ const char* fa_last_error_string(void);
  * word that kernels set when a bounded wait ran out.  *code (may be NULL)
  * receives the raw word (kernel id << 24 | wait site << 16 | block), the
  * kernel id being one of FA_ERRWORD_*.  Returns FA_OK if it was clear,
- * FA_ERR_TIMEOUT if set, FA_ERR_CUDA if the synchronisation failed. */
-enum { FA_ERRWORD_FWD = 1, FA_ERRWORD_BWD_D64 = 3, FA_ERRWORD_BWD_D128 = 4 };
+ * FA_ERR_TIMEOUT if set, FA_ERR_CUDA if the synchronisation failed;
+ * FA_ERR_BAD_PAGE for the id FA_ERRWORD_CACHE_PAGE, whose low 16 bits are the
+ * sequence's number and whose wait site says what was wrong: 1 a context
+ * length, 2 / 4 / 6 / 7 a page id or slot (attention / append / compact source /
+ * compact target), 3 / 5 a count (append / compact).  The first error since
+ * the last call is the one that is kept. */
+enum {
+  FA_ERRWORD_FWD = 1,
+  FA_ERRWORD_BWD_D64 = 3,
+  FA_ERRWORD_BWD_D128 = 4,
+  FA_ERRWORD_CACHED = 5,
+  FA_ERRWORD_CACHE_PAGE = 6
+};
 fa_status fa_device_error(unsigned int* code);
 
 /* Test hooks for the bounded-wait exit path (the pages have no counterpart;
