@@ -226,15 +226,85 @@ struct BwdParams {
 struct ViewStrides {
   long long b, h, n;
 };
-// The windowed forms of the main kernels (WIN): an item is a 128-key block of
-// one *key* head, and its query blocks are those that see its keys, of every
-// query head that shares it, one head after the other -- so dK and dV of a
-// shared head are summed in the accumulators.  BH counts key heads (B * Hkv).
+// The windowed forms of the main kernels (WIN): the work of a 128-key block of
+// one *key* head is the query blocks that see its keys, of every query head
+// that shares it, one head after the other -- so dK and dV of a shared head are
+// summed in the accumulators.  BH counts key heads (B * Hkv).  Sink blocks are
+// seen by every later query and so are far longer than the others, and a few
+// shared heads may be too few items for the SMs: the steps of a block are cut
+// into pieces (ps of them for a sink block, pw for another; the host's rule is in
+// window_pieces) and an item is one piece.  Where there is more than one, each
+// writes its fp32 dK and dV to a place of its own and the convert kernel adds
+// them in order, so the result does not depend on which finished first.
 struct BwdWinParams : BwdParams {
   WindowShape w;
+  int ps, pw;
   ViewStrides dk_strides, dv_strides;
+  float* kv_part;  // [pieces][dV, dK][128][D]
 };
 template <bool WIN>
 using BwdArgs = std::conditional_t<WIN, BwdWinParams, BwdParams>;
+
+// Place of a piece's partial dV, dK (in units of 2 * 128 * D floats); the sink
+// blocks' come first.  Only blocks of several pieces have places.
+struct WindowPieces {
+  int ps, pw, nsb, n_blk;
+  __host__ __device__ __forceinline__ int of(int kb) const { return kb < nsb ? ps : pw; }
+  __host__ __device__ __forceinline__ long long place(int bh, int BH, int kb, int piece) const {
+    const long long sinks = ps > 1 ? static_cast<long long>(BH) * nsb * ps : 0;
+    if (kb < nsb) return (static_cast<long long>(bh) * nsb + kb) * ps + piece;
+    return sinks + (static_cast<long long>(bh) * (n_blk - nsb) + (kb - nsb)) * pw + piece;
+  }
+  __host__ __device__ __forceinline__ long long places(int BH) const {
+    return (ps > 1 ? static_cast<long long>(BH) * nsb * ps : 0) +
+           (pw > 1 ? static_cast<long long>(BH) * (n_blk - nsb) * pw : 0);
+  }
+};
+
+// One item of the windowed backward: n steps of key block kblk.
+struct BwdWinItem {
+  int kblk, bh, piece, nq, n;
+  int q0, h0;  // query block (from kblk) and head (of the group) of the first step
+  // item number w of the sink blocks' list (SINK) or the others', over `heads`
+  // key heads from `first` on: key blocks in order, of each the pieces, of each
+  // the heads
+  template <bool SINK>
+  __device__ __forceinline__ void load(const BwdWinParams& p, int w, int first, int heads) {
+    const int pieces = SINK ? p.ps : p.pw;
+    kblk = SINK ? 0 : p.w.n_sink_blk;
+    int q = w / heads;  // (key block, piece)
+    bh = first + (w - q * heads);
+    piece = 0;
+    if (pieces > 1) {
+      const int kb = q / pieces;
+      piece = q - kb * pieces;
+      q = kb;
+    }
+    kblk += q;
+    nq = p.w.last_query_block(kblk, p.n_blk) - kblk + 1;
+    n = nq * p.w.G;  // (G * n_blk is below 2^31, as the whole problem's blocks are)
+    q0 = h0 = 0;
+    if (pieces > 1) {  // the first n % pieces of them are one step longer
+      const int len = n / pieces, longer = n - len * pieces;
+      const int k0 = len * piece + (piece < longer ? piece : longer);
+      n = len + (piece < longer ? 1 : 0);
+      h0 = k0 / nq;
+      q0 = k0 - h0 * nq;
+    }
+  }
+  __device__ __forceinline__ static int sinks(const BwdWinParams& p) { return p.w.n_sink_blk * p.ps * p.BH; }
+  __device__ __forceinline__ static int others(const BwdWinParams& p, int heads) {
+    return (p.n_blk - p.w.n_sink_blk) * p.pw * heads;
+  }
+};
+
+// 32 columns of this thread's row of a partial dV or dK
+__device__ __forceinline__ void store_part32(float* dst, const uint32_t (&r)[32], float f) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 4)
+    *reinterpret_cast<float4*>(dst + c) =
+        make_float4(__uint_as_float(r[c]) * f, __uint_as_float(r[c + 1]) * f, __uint_as_float(r[c + 2]) * f,
+                    __uint_as_float(r[c + 3]) * f);
+}
 
 }  // namespace fa

@@ -110,50 +110,63 @@ struct BwdCursor {
   int c, G, W, BH, n_blk, causal;
   int r, kblk, bh, n, i0, i;
   bool valid;
-  // WIN: the window, query blocks per head, flat index of the first query head
-  std::conditional_t<WIN, WindowShape, int> win;
-  int nq, bh0;
+  // WIN: query blocks per head, number of the piece; query block (from kblk) and flat query head of the current step
+  std::conditional_t<WIN, BwdWinParams, char> args;
+  int nq, piece, qi, hi;
   __device__ __forceinline__ void load() {
     const int w = r * G + ((r & 1) ? (G - 1 - c) : c);
     valid = w < W;
-    if (valid) {
+    if constexpr (WIN) {
+      if (valid) {
+        BwdWinItem it{};
+        const int sinks = BwdWinItem::sinks(args);
+        if (w < sinks)
+          it.load<true>(args, w, 0, BH);
+        else
+          it.load<false>(args, w - sinks, 0, BH);
+        kblk = it.kblk;
+        bh = it.bh;
+        n = it.n;
+        i0 = it.kblk;
+        i = 0;
+        nq = it.nq;
+        piece = it.piece;
+        qi = it.q0;
+        hi = bh * args.w.G + it.h0;  // flat key head b * Hkv + hk -> flat query head b * H + hk * G
+      }
+    } else if (valid) {
       kblk = w / BH;
       bh = w - kblk * BH;
       n = causal ? (n_blk - kblk) : n_blk;
       i0 = causal ? kblk : 0;
       i = 0;
-      if constexpr (WIN) {
-        nq = win.last_query_block(kblk, n_blk) - kblk + 1;
-        n = nq * win.G;
-        bh0 = bh * win.G;  // B-major: flat key head b * Hkv + hk -> flat query head b * H + hk * G
+    }
+  }
+  // WIN: on to the item's next step
+  __device__ __forceinline__ void advance() {
+    if constexpr (WIN) {
+      if (++qi == nq) {
+        qi = 0;
+        ++hi;
       }
     }
   }
-  // query block and flat query head of the item's step k
-  __device__ __forceinline__ int qblk_of(int k) const {
-    if constexpr (WIN)
-      return i0 + k % nq;
-    else
-      return i0 + k;
-  }
-  __device__ __forceinline__ int head_of(int k) const {
-    if constexpr (WIN)
-      return bh0 + k / nq;
-    else
-      return bh;
-  }
   __device__ __forceinline__ void start(const BwdArgs<WIN>& p) {
-    if constexpr (WIN) win = p.w;
+    if constexpr (WIN) args = p;
     c = blockIdx.x;
     G = gridDim.x;
     BH = p.BH;
     n_blk = p.n_blk;
-    W = p.n_blk * p.BH;
+    if constexpr (WIN)
+      W = BwdWinItem::sinks(p) + BwdWinItem::others(p, p.BH);
+    else
+      W = p.n_blk * p.BH;
     causal = p.causal;
     r = 0;
     load();
   }
   __device__ __forceinline__ void next_block() {
+    advance();
     if (++i >= n) {
       ++r;
       load();
@@ -163,8 +176,18 @@ struct BwdCursor {
     ++r;
     load();
   }
-  __device__ __forceinline__ int qblk() const { return qblk_of(i); }
-  __device__ __forceinline__ int head() const { return head_of(i); }
+  __device__ __forceinline__ int qblk() const {
+    if constexpr (WIN)
+      return i0 + qi;
+    else
+      return i0 + i;
+  }
+  __device__ __forceinline__ int head() const {
+    if constexpr (WIN)
+      return hi;
+    else
+      return bh;
+  }
 };
 
 template <bool WIN = false>
@@ -260,10 +283,10 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
       auto load_q = [&](int i, int gq) {
         const int s = gq % NST, use = gq / NST;
         if (use > 0 && !wait(bar(L::Q_EMPTY + s), (use - 1) & 1, 1)) return false;
-        const int row0 = cur.qblk_of(i) * L::B;
+        const int row0 = (WIN ? cur.qblk() : cur.i0 + i) * L::B;
         mbar_expect_tx(bar(L::Q_FULL + s), 2 * TILE);
         if constexpr (WIN) {
-          const int f = cur.head_of(i), b = f / p.w.H, h = f - b * p.w.H;
+          const int f = cur.head(), b = f / p.w.H, h = f - b * p.w.H;
           tma_load_4d(base + L::Q_OFF + s * TILE, &tm_q, bar(L::Q_FULL + s), 0, row0, h, b);
           tma_load_4d(base + L::DO_OFF + s * TILE, &tm_do, bar(L::Q_FULL + s), 0, row0, h, b);
         } else {
@@ -271,6 +294,7 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
           tma_load_3d(base + L::DO_OFF + s * TILE, &tm_do, bar(L::Q_FULL + s), 0, row0, cur.bh);
         }
         issued[s] = gq;
+        cur.advance();  // (steps are loaded in order)
         return true;
       };
       bool ok = true;
@@ -537,7 +561,7 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     bool ok = true;
     const bool stall = inject_stall_here(3u);  // test hook (fa_debug_inject_stall)
     for (; cur.valid; cur.next_item()) {
-      for (int i = 0; i < cur.n; ++i, ++g) {
+      for (int i = 0; i < cur.n; ++i, ++g, cur.advance()) {
         const int b = g & 1;
         ok = ok && wait.warp(bar(L::VEC_FULL + b), (g >> 1) & 1, 8);
         ok = ok && wait.warp(bar(L::S_FULL + b), (g >> 1) & 1, 9);
@@ -549,7 +573,7 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         uint32_t vis[2] = {0xffffffffu, 0xffffffffu};  // WIN: queries of this half that see key t
         bool part = false;                             // WIN: some pair of the two blocks is hidden
         if constexpr (WIN) {
-          const int qb = cur.qblk_of(i);
+          const int qb = cur.qblk();
           part = !p.w.block_full(qb, cur.kblk);
           const RowMask mk = p.w.column_mask(cur.kblk * L::B + t, qb * L::B + qoff);
           vis[0] = mk.word(0);
@@ -680,6 +704,19 @@ fa_bwd_main_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
       tmem_ld32x2(tmem + lane_base + col, tmem + lane_base + col + 32, r0, r1);
       tc_fence_before();
       mbar_arrive(bar(L::ACC_FREE));  // the next item may overwrite the accumulators
+      if constexpr (WIN) {
+        // a piece of several: fp32 to its own place
+        const WindowPieces pc{p.ps, p.pw, p.w.n_sink_blk, p.n_blk};
+        if (pc.of(cur.kblk) > 1) {
+          float* dst = p.kv_part + ((pc.place(cur.bh, p.BH, cur.kblk, cur.piece) * 2 + h) * 128 + t) * 64;
+          if (ok) {
+            store_part32(dst, r0, f);
+            store_part32(dst + 32, r1, f);
+          }
+          if (!named_barrier_and(1, 256, ok)) break;
+          continue;
+        }
+      }
       uint32_t w[32];
 #pragma unroll
       for (int c = 0; c < 16; ++c) {

@@ -113,6 +113,21 @@ __device__ __forceinline__ void bwd_item_decode(const BwdParams& p, int w, int& 
   bh = first + (lw - kblk * hg);
 }
 
+// The same for the windowed form: the sink blocks of all heads, which are the
+// longest items, and then the others in groups.
+__device__ __forceinline__ void bwd_item_decode(const BwdWinParams& p, int w, BwdWinItem& it) {
+  const int sinks = BwdWinItem::sinks(p);
+  if (w < sinks) {
+    it.load<true>(p, w, 0, p.BH);
+    return;
+  }
+  w -= sinks;
+  const int per_group = BwdWinItem::others(p, p.head_group);
+  const int gi = w / per_group, lw = w - gi * per_group;
+  const int first = gi * p.head_group;
+  it.load<false>(p, lw, first, (p.BH - first) < p.head_group ? (p.BH - first) : p.head_group);
+}
+
 // Items of one CTA, taken from a list shared by all CTAs: the producer thread
 // claims the next item number with an atomic add on a counter in the
 // workspace (so CTAs that finish early take more items) and publishes it, one
@@ -126,7 +141,7 @@ struct RingCursor {
   BwdArgs<WIN> p;
   int r, kblk, bh, n, i0, i;
   bool valid;
-  int nq;  // WIN: query blocks per query head
+  int nq, piece, qi, hi;  // WIN: as in BwdCursor
   __device__ __forceinline__ void load() {
     const int slot = r & 3;
     const bool got = uniform ? wt.warp(full + 8u * slot, (r >> 2) & 1, 40) : wt(full + 8u * slot, (r >> 2) & 1, 40);
@@ -136,28 +151,32 @@ struct RingCursor {
     asm volatile("ld.shared.s32 %0, [%1];" : "=r"(w) : "r"(ring + 4u * slot) : "memory");
     mbar_arrive(empty + 8u * slot);
     if (w < 0) return;
-    bwd_item_decode(p, w, kblk, bh);
-    n = p.causal ? (p.n_blk - kblk) : p.n_blk;
-    i0 = p.causal ? kblk : 0;
-    i = 0;
     if constexpr (WIN) {
-      nq = p.w.last_query_block(kblk, p.n_blk) - kblk + 1;
-      n = nq * p.w.G;
+      BwdWinItem it;
+      bwd_item_decode(p, w, it);
+      kblk = it.kblk;
+      bh = it.bh;
+      n = it.n;
+      i0 = it.kblk;
+      nq = it.nq;
+      piece = it.piece;
+      qi = it.q0;
+      hi = bh * p.w.G + it.h0;
+    } else {
+      bwd_item_decode(p, w, kblk, bh);
+      n = p.causal ? (p.n_blk - kblk) : p.n_blk;
+      i0 = p.causal ? kblk : 0;
     }
+    i = 0;
     valid = true;
   }
-  // query block and flat query head of the item's step k (as in BwdCursor)
-  __device__ __forceinline__ int qblk_of(int k) const {
-    if constexpr (WIN)
-      return i0 + k % nq;
-    else
-      return i0 + k;
-  }
-  __device__ __forceinline__ int head_of(int k) const {
-    if constexpr (WIN)
-      return bh * p.w.G + k / nq;
-    else
-      return bh;
+  __device__ __forceinline__ void advance() {
+    if constexpr (WIN) {
+      if (++qi == nq) {
+        qi = 0;
+        ++hi;
+      }
+    }
   }
   __device__ __forceinline__ void start() {
     r = 0;
@@ -167,6 +186,7 @@ struct RingCursor {
   // end marker is never published (the vector prefetch cursor, which runs two
   // blocks ahead, keeps advancing after the end).
   __device__ __forceinline__ void next_block() {
+    advance();
     if (valid && ++i >= n) {
       ++r;
       load();
@@ -177,8 +197,18 @@ struct RingCursor {
     ++r;
     load();
   }
-  __device__ __forceinline__ int qblk() const { return qblk_of(i); }
-  __device__ __forceinline__ int head() const { return head_of(i); }
+  __device__ __forceinline__ int qblk() const {
+    if constexpr (WIN)
+      return i0 + qi;
+    else
+      return i0 + i;
+  }
+  __device__ __forceinline__ int head() const {
+    if constexpr (WIN)
+      return hi;
+    else
+      return bh;
+  }
 };
 
 template <bool WIN = false>
@@ -262,9 +292,13 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       struct PItem {
         int r, kblk, bh, n, i0;
         bool valid;
-        int nq;
+        int nq, qi, hi;
       };
-      const int W = p.n_blk * p.BH;
+      int W;
+      if constexpr (WIN)
+        W = BwdWinItem::sinks(p) + BwdWinItem::others(p, p.BH);
+      else
+        W = p.n_blk * p.BH;
       auto publish = [&](int r, PItem& it) -> bool {
         const int slot = r & 3;
         if (r >= L::RING && !wait(bar(L::ITEM_EMPTY + slot), ((r - L::RING) >> 2) & 1, 41)) return false;
@@ -275,12 +309,20 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         it.r = r;
         it.valid = v >= 0;
         if (it.valid) {
-          bwd_item_decode(p, v, it.kblk, it.bh);
-          it.n = p.causal ? (p.n_blk - it.kblk) : p.n_blk;
-          it.i0 = p.causal ? it.kblk : 0;
           if constexpr (WIN) {
-            it.nq = p.w.last_query_block(it.kblk, p.n_blk) - it.kblk + 1;
-            it.n = it.nq * p.w.G;
+            BwdWinItem wi;
+            bwd_item_decode(p, v, wi);
+            it.kblk = wi.kblk;
+            it.bh = wi.bh;
+            it.n = wi.n;
+            it.i0 = wi.kblk;
+            it.nq = wi.nq;
+            it.qi = wi.q0;
+            it.hi = wi.bh * p.w.G + wi.h0;
+          } else {
+            bwd_item_decode(p, v, it.kblk, it.bh);
+            it.n = p.causal ? (p.n_blk - it.kblk) : p.n_blk;
+            it.i0 = p.causal ? it.kblk : 0;
           }
         }
         return true;
@@ -292,11 +334,11 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       auto load_q = [&](int i, int gq) {
         const int s = gq % NST, use = gq / NST;
         if (use > 0 && !wait(bar(L::Q_EMPTY + s), (use - 1) & 1, 1)) return false;
-        const int row0 = (WIN ? cur.i0 + i % cur.nq : cur.i0 + i) * L::B;
+        const int row0 = (cur.i0 + (WIN ? cur.qi : i)) * L::B;
         const uint32_t qd = base + L::Q_OFF + s * TILE, dod = base + L::DO_OFF + s * TILE;
         mbar_expect_tx(bar(L::Q_FULL + s), 2 * TILE);
         if constexpr (WIN) {
-          const int f = cur.bh * p.w.G + i / cur.nq, b = f / p.w.H, hd = f - b * p.w.H;
+          const int f = cur.hi, b = f / p.w.H, hd = f - b * p.w.H;
           for (int h = 0; h < 2; ++h) {
             tma_load_4d(qd + h * HALF, &tm_q, bar(L::Q_FULL + s), 64 * h, row0, hd, b);
             tma_load_4d(dod + h * HALF, &tm_do, bar(L::Q_FULL + s), 64 * h, row0, hd, b);
@@ -308,6 +350,10 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
           }
         }
         issued[s] = gq;
+        if (WIN && ++cur.qi == cur.nq) {  // (steps are loaded in order)
+          cur.qi = 0;
+          ++cur.hi;
+        }
         return true;
       };
       bool ok = publish(0, cur);
@@ -567,7 +613,7 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
     const bool stall = inject_stall_here(4u);  // test hook (fa_debug_inject_stall)
     for (; cur.valid; cur.next_item()) {
       bool leave = false;
-      for (int i = 0; i < cur.n; ++i, ++g) {
+      for (int i = 0; i < cur.n; ++i, ++g, cur.advance()) {
         // this warpgroup has finished with the previous block's vectors
         named_barrier_sync(3 + h, 128);
         if (vrole == 0) {
@@ -593,7 +639,7 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
         uint32_t vis[2] = {0xffffffffu, 0xffffffffu};  // WIN: queries of this half that see key t
         bool part = false;                             // WIN: some pair of the two blocks is hidden
         if constexpr (WIN) {
-          const int qb = cur.qblk_of(i);
+          const int qb = cur.qblk();
           part = !p.w.block_full(qb, cur.kblk);
           const RowMask mk = p.w.column_mask(cur.kblk * L::B + t, qb * L::B + qoff);
           vis[0] = mk.word(0);
@@ -708,7 +754,11 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
       const int key = cur.kblk * L::B + t;
       const bool row_ok = ok && key < p.N;
       __nv_bfloat16* dst = h == 0 ? p.dv : p.dk;
+      float* part = nullptr;  // WIN, a piece of several: fp32 to its own place
       if constexpr (WIN) {
+        const WindowPieces pc{p.ps, p.pw, p.w.n_sink_blk, p.n_blk};
+        if (pc.of(cur.kblk) > 1)
+          part = p.kv_part + ((pc.place(cur.bh, p.BH, cur.kblk, cur.piece) * 2 + h) * 128 + t) * L::D;
         const ViewStrides& st = h == 0 ? p.dv_strides : p.dk_strides;
         const int hkv = p.w.H / p.w.G, b = cur.bh / hkv;
         dst += b * st.b + (cur.bh - b * hkv) * st.h + (row_ok ? key : 0) * st.n;
@@ -723,7 +773,12 @@ fa_bwd_main_pipe128_kernel(const __grid_constant__ CUtensorMap tm_q, const __gri
           tc_fence_before();
           mbar_arrive(bar(L::ACC_FREE));  // the next item may overwrite the accumulators
         }
-        if (row_ok) {
+        if (WIN && part != nullptr) {
+          if (ok) {
+            store_part32(part + 64 * half, r0, f);
+            store_part32(part + 64 * half + 32, r1, f);
+          }
+        } else if (row_ok) {
 #pragma unroll
           for (int c = 0; c < 32; c += 8) {
             uint4 w0, w1;

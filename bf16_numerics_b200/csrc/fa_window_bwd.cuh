@@ -64,43 +64,87 @@ fa_window_delta_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16*
   }
 }
 
-// dq = bf16(dq_acc): tiles of 8192 elements of one head (256 threads, four
-// chunks of 8 elements each, loads first).
+// dq = bf16(dq_acc), and dk, dv of the key blocks that were worked on in pieces
+// = bf16(sum of the pieces, in order).  Tiles of 8192 elements of one head (256
+// threads, four chunks of 8 elements each, loads first): the dq tiles, then two
+// sets (dV, dK) of 128 * D / 8192 tiles per key block in pieces.
+struct ConvertParams {
+  const float* dq_acc;
+  const float* kv_part;
+  __nv_bfloat16 *dq, *dk, *dv;
+  ViewStrides sdq, sdk, sdv;
+  int H, Hkv, BHk, N;
+  long long dq_tiles, tiles;
+  int dq_tiles_per_head;
+  int first_blk, n_blk_pieces;  // the key blocks in pieces: [first_blk, first_blk + n_blk_pieces)
+  WindowPieces pieces;
+};
 template <int D>
 __global__ void __launch_bounds__(256)
-fa_window_dq_convert_kernel(const float* __restrict__ dq_acc, __nv_bfloat16* __restrict__ dq, ViewStrides sdq, int H,
-                            int N, long long tiles, int tiles_per_head) {
-  constexpr int U = 4, CPR = D / 8;         // chunks per row
-  constexpr int ROWS = 256 * U / CPR;       // rows per tile
-  grid_dependency_wait();  // the accumulator is complete once the main grid is
-  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const long long bh = tile / tiles_per_head;
-    const int n0 = static_cast<int>(tile - bh * tiles_per_head) * ROWS;
-    const long long b = bh / H;
-    const int h = static_cast<int>(bh - b * H);
-    const float4* src = reinterpret_cast<const float4*>(dq_acc + bh * N * D);
-    __nv_bfloat16* dst = dq + b * sdq.b + h * sdq.h;
+fa_window_convert_kernel(const ConvertParams p) {
+  constexpr int U = 4, CPR = D / 8;    // chunks per row
+  constexpr int ROWS = 256 * U / CPR;  // rows per tile
+  constexpr int TPB = 128 / ROWS;      // tiles per key block
+  grid_dependency_wait();  // the accumulator and the pieces are complete once the main grid is
+  for (long long tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    const float4* src;     // row n0 of what is converted
+    __nv_bfloat16* dst;    // the same row of the output
+    long long dst_n;       // its row stride
+    int n0, parts = 1;
+    if (tile < p.dq_tiles) {
+      const long long bh = tile / p.dq_tiles_per_head, b = bh / p.H;
+      n0 = static_cast<int>(tile - bh * p.dq_tiles_per_head) * ROWS;
+      src = reinterpret_cast<const float4*>(p.dq_acc + (bh * p.N + n0) * D);
+      dst = p.dq + b * p.sdq.b + (bh - b * p.H) * p.sdq.h;
+      dst_n = p.sdq.n;
+    } else {
+      long long x = tile - p.dq_tiles;
+      const int sub = static_cast<int>(x % TPB);
+      x /= TPB;
+      const int which = static_cast<int>(x & 1);  // 0: dV, 1: dK
+      x >>= 1;
+      const int bh = static_cast<int>(x / p.n_blk_pieces), kb = p.first_blk + static_cast<int>(x % p.n_blk_pieces);
+      const int b = bh / p.Hkv;
+      const ViewStrides& st = which == 0 ? p.sdv : p.sdk;
+      n0 = kb * 128 + sub * ROWS;
+      parts = p.pieces.of(kb);
+      src = reinterpret_cast<const float4*>(
+          p.kv_part + ((p.pieces.place(bh, p.BHk, kb, 0) * 2 + which) * 128 + sub * ROWS) * D);
+      dst = (which == 0 ? p.dv : p.dk) + b * st.b + (bh - b * p.Hkv) * st.h;
+      dst_n = st.n;
+    }
     float4 x[U], y[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = threadIdx.x + 256 * u;
-      const long long n = n0 + i / CPR;
-      if (n < N) {
-        x[u] = __ldcs(src + n * (D / 4) + 2 * (i % CPR));
-        y[u] = __ldcs(src + n * (D / 4) + 2 * (i % CPR) + 1);
+      if (n0 + i / CPR < p.N) {
+        x[u] = __ldcs(src + 2 * i);
+        y[u] = __ldcs(src + 2 * i + 1);
+      }
+    }
+    for (int k = 1; k < parts; ++k) {
+      src += 2 * 128 * D / 4;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = threadIdx.x + 256 * u;
+        if (n0 + i / CPR < p.N) {
+          const float4 a = __ldcs(src + 2 * i), c = __ldcs(src + 2 * i + 1);
+          x[u].x += a.x; x[u].y += a.y; x[u].z += a.z; x[u].w += a.w;
+          y[u].x += c.x; y[u].y += c.y; y[u].z += c.z; y[u].w += c.w;
+        }
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = threadIdx.x + 256 * u;
       const long long n = n0 + i / CPR;
-      if (n < N) {
+      if (n < p.N) {
         uint4 w;
         w.x = pack_bf16x2(x[u].x, x[u].y);
         w.y = pack_bf16x2(x[u].z, x[u].w);
         w.z = pack_bf16x2(y[u].x, y[u].y);
         w.w = pack_bf16x2(y[u].z, y[u].w);
-        *reinterpret_cast<uint4*>(dst + n * sdq.n + 8 * (i % CPR)) = w;
+        *reinterpret_cast<uint4*>(dst + n * dst_n + 8 * (i % CPR)) = w;
       }
     }
   }

@@ -124,16 +124,84 @@ fa_status launch_window_fwd(const fa_view* q, const fa_view* k, const fa_view* v
   return e == cudaSuccess ? FA_OK : cuda_fail("fa_window_fwd launch", e);
 }
 
-// workspace: delta | fp32 dQ accumulator | work-item counter
+int sm_count_or_default() {
+  const int n = sm_count();
+  return n > 0 ? n : 148;
+}
+// How the backward's steps (128 x 128 block products) are cut into items.  A
+// sink block has up to G * n_blk steps and another up to G * (window / 128 + 2);
+// long items are waited for, many short ones pay for their ends.  For a series
+// of longest pieces the time of the busiest SM is estimated -- an item costs its
+// steps and two more, three if its result goes to a partial's place (K and V
+// loads, first products and the epilogue do not overlap); the sink pieces go
+// first, round by round, and each of the others to the SM that is free first; an
+// eighth of the longest item stands for the spread -- and the smallest wins.
+// Measured (forward + backward, one B200, pieces of a sink and of another block):
+// N 4096, 8 heads over 1, d 128, window 512, sinks 4: 945 us uncut, 127 us with
+// (22, 4), 155 with (32, 5), 148 with (11, 2); N 8192, 2 x 16 heads over 4, d 128,
+// window 1024: 1600 us uncut, 955 us with (2, 1), 894 with (4, 1), 962 with (8, 2).
+fa::WindowPieces window_pieces(int B, int H, int Hkv, int N, int window, int sinks, int n_sm) {
+  constexpr long long kUnit = 16;  // times in sixteenths of a step
+  const fa::WindowShape w = window_shape(H, Hkv, N, window, sinks);
+  fa::WindowPieces best{1, 1, w.n_sink_blk, (N + 127) / 128};
+  const long long n_blk = best.n_blk, nsb = best.nsb, G = w.G, BHk = static_cast<long long>(B) * Hkv;
+  const long long rest = n_blk - nsb;
+  const long long reach = (126ll + w.window) / 128 + 1;  // query blocks that see a block away from the row's end
+  const long long wide = reach < rest ? reach : rest;    // .. the last ones: wide, wide - 1, .., 1
+  const long long sink_steps = (nsb * n_blk - nsb * (nsb - 1) / 2) * G * BHk;
+  const long long rest_steps = ((rest - wide) * wide + wide * (wide + 1) / 2) * G * BHk;
+  const long long top = nsb > 0 ? G * n_blk : G * wide;
+  long long best_time = -1;
+  for (long long most = 4;; most += (most + 3) / 4) {
+    auto cut = [&](long long steps, long long fewest) {
+      const long long k = (steps + most - 1) / most;
+      return k < 1 ? 1 : (k < fewest ? k : fewest);  // no piece without a step
+    };
+    const long long ps = nsb > 0 ? cut(G * n_blk, G * (n_blk - nsb + 1)) : 1, pw = rest > 0 ? cut(G * wide, G) : 1;
+    // items of each kind, their mean cost and the longest one's
+    const long long is = nsb * ps * BHk, iw = rest * pw * BHk;
+    const long long es = (ps > 1 ? 3 : 2) * kUnit, ew = (pw > 1 ? 3 : 2) * kUnit;
+    const long long ms = is > 0 ? sink_steps * kUnit / is + es : 1, mw = iw > 0 ? rest_steps * kUnit / iw + ew : 1;
+    const long long ls = is > 0 ? G * n_blk * kUnit / ps + es : 0, lw = iw > 0 ? G * wide * kUnit / pw + ew : 0;
+    const long long rounds = is / n_sm, more = is - rounds * n_sm;  // `more` SMs take one sink piece more
+    const long long free_a = (rounds + 1) * ms, free_b = rounds * ms;
+    auto started = [&](long long t) {  // others that have been started at time t
+      return (t >= free_a ? ((t - free_a) / mw + 1) * more : 0) + (t >= free_b ? ((t - free_b) / mw + 1) * (n_sm - more) : 0);
+    };
+    long long lo = 0, hi = free_a + (iw / n_sm + 1) * mw;
+    while (lo < hi) {  // when the last one starts
+      const long long t = lo + (hi - lo) / 2;
+      if (started(t) >= iw)
+        hi = t;
+      else
+        lo = t + 1;
+    }
+    const long long longest = ls > lw ? ls : lw, sinks_end = more > 0 ? free_a : free_b;
+    long long time = iw > 0 ? lo + lw : 0;
+    if (time < sinks_end) time = sinks_end;
+    if (time < longest) time = longest;
+    time += longest / 8;
+    if (best_time < 0 || time <= best_time) {  // of equals the fewest pieces
+      best_time = time;
+      best.ps = static_cast<int>(ps);
+      best.pw = static_cast<int>(pw);
+    }
+    if (most >= top) break;
+  }
+  return best;
+}
+
+// workspace: delta | fp32 dQ accumulator | work-item counter | partial dV, dK
 struct WindowBwdLayout {
-  size_t acc_off, ctr_off, bytes;
+  size_t acc_off, ctr_off, part_off, bytes;
 };
-WindowBwdLayout window_bwd_layout(int B, int H, int N, int d) {
+WindowBwdLayout window_bwd_layout(int B, int H, int Hkv, int N, int d, const fa::WindowPieces& pc) {
   const size_t rows = static_cast<size_t>(B) * H * N;
   WindowBwdLayout l{};
   l.acc_off = round256(rows * 4);
   l.ctr_off = l.acc_off + rows * d * 4;  // a multiple of 256 past acc_off
-  l.bytes = l.ctr_off + 256;
+  l.part_off = l.ctr_off + 256;
+  l.bytes = l.part_off + static_cast<size_t>(pc.places(B * Hkv)) * 2 * 128 * d * 4;
   return l;
 }
 
@@ -151,7 +219,8 @@ fa_status launch_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v
   const int n_sm = sm_count();
   if (n_sm <= 0) return cuda_fail("cudaDeviceGetAttribute(multiprocessor count)");
   const int BH = B * H, n_blk = (N + 127) / 128;
-  const WindowBwdLayout wl = window_bwd_layout(B, H, N, D);
+  const fa::WindowPieces pieces = window_pieces(B, H, Hkv, N, window, sinks, n_sm);
+  const WindowBwdLayout wl = window_bwd_layout(B, H, Hkv, N, D, pieces);
   float* delta = reinterpret_cast<float*>(ws);
   float* dq_acc = reinterpret_cast<float*>(ws + wl.acc_off);
   CUtensorMap mq, mk, mv, mdo, mdq, mdk, mdv;
@@ -164,7 +233,7 @@ fa_status launch_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v
     constexpr int rows_per_group = 2 * 32 / (D / 8);
     const int per_head = (N + rows_per_group - 1) / rows_per_group;
     const long long groups = static_cast<long long>(BH) * per_head;
-    const long long clear4 = static_cast<long long>(wl.bytes - wl.acc_off) / 16;
+    const long long clear4 = static_cast<long long>(wl.part_off - wl.acc_off) / 16;
     const dim3 grid(grid_for(groups, 4));
     const int clear_blocks = delta_clear_blocks(static_cast<int>(grid.x), clear4 * 16);
     LaunchTimer tm(FA_KERNEL_BWD_DELTA, stream);
@@ -194,12 +263,16 @@ fa_status launch_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v
     p.w = window_shape(H, Hkv, N, window, sinks);
     p.dk_strides = strides_of(dk);
     p.dv_strides = strides_of(dv);
+    p.ps = pieces.ps;
+    p.pw = pieces.pw;
+    p.kv_part = reinterpret_cast<float*>(ws + wl.part_off);
     // d = 128 item order: key heads in groups whose fp32 dQ rows fit in 32 MB (see launch_bwd)
     const long long per_head = static_cast<long long>(N) * D * 4 * p.w.G;
     long long hg = (32ll << 20) / per_head;
     hg = hg < 1 ? 1 : (hg > p.BH ? p.BH : hg);
     p.head_group = static_cast<int>(hg);
-    const long long items = static_cast<long long>(n_blk) * p.BH;
+    const long long items =
+        (static_cast<long long>(p.w.n_sink_blk) * p.ps + static_cast<long long>(n_blk - p.w.n_sink_blk) * p.pw) * p.BH;
     const dim3 grid(static_cast<unsigned>(items < n_sm ? items : n_sm));
     LaunchTimer tm(FA_KERNEL_BWD_MAIN, stream);
     cudaError_t e;
@@ -218,15 +291,30 @@ fa_status launch_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v
   }
   {
     constexpr int rows_per_tile = 8192 / D;
-    const int per_head = (N + rows_per_tile - 1) / rows_per_tile;
-    const long long tiles = static_cast<long long>(BH) * per_head;
+    fa::ConvertParams p{};
+    p.dq_acc = dq_acc;
+    p.kv_part = reinterpret_cast<const float*>(ws + wl.part_off);
+    p.dq = static_cast<__nv_bfloat16*>(dq->ptr);
+    p.dk = static_cast<__nv_bfloat16*>(dk->ptr);
+    p.dv = static_cast<__nv_bfloat16*>(dv->ptr);
+    p.sdq = strides_of(dq);
+    p.sdk = strides_of(dk);
+    p.sdv = strides_of(dv);
+    p.H = H;
+    p.Hkv = Hkv;
+    p.BHk = B * Hkv;
+    p.N = N;
+    p.dq_tiles_per_head = (N + rows_per_tile - 1) / rows_per_tile;
+    p.dq_tiles = static_cast<long long>(BH) * p.dq_tiles_per_head;
+    p.pieces = pieces;
+    p.first_blk = pieces.ps > 1 ? 0 : pieces.nsb;
+    p.n_blk_pieces = (pieces.pw > 1 ? n_blk : pieces.nsb) - p.first_blk;
+    p.tiles = p.dq_tiles + static_cast<long long>(p.BHk) * p.n_blk_pieces * 2 * (128 / rows_per_tile);
     LaunchTimer tm(FA_KERNEL_BWD_DQ, stream);
-    cudaError_t e = launch_pdl(fa::fa_window_dq_convert_kernel<D>, dim3(grid_for(tiles, 1)), dim3(256), 0, stream,
-                               static_cast<const float*>(dq_acc), static_cast<__nv_bfloat16*>(dq->ptr),
-                               strides_of(dq), H, N, tiles, per_head);
+    cudaError_t e = launch_pdl(fa::fa_window_convert_kernel<D>, dim3(grid_for(p.tiles, 1)), dim3(256), 0, stream, p);
     tm.done();
     if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail("fa_window_dq_convert_kernel launch", e);
+    if (e != cudaSuccess) return cuda_fail("fa_window_convert_kernel launch", e);
   }
   return FA_OK;
 }
@@ -258,7 +346,8 @@ fa_status fa_window_fwd(const fa_view* q, const fa_view* k, const fa_view* v, co
 size_t fa_window_bwd_workspace_bytes(int B, int H, int Hkv, int N, int d, int window, int sinks) {
   bool empty = false;
   if (window_args(B, H, Hkv, N, d, window, sinks, FA_SOFTMAX_STANDARD, 0.f, &empty) != FA_OK) return 0;
-  return window_bwd_layout(B, H, N, d).bytes;
+  if (empty) return 256;
+  return window_bwd_layout(B, H, Hkv, N, d, window_pieces(B, H, Hkv, N, window, sinks, sm_count_or_default())).bytes;
 }
 
 fa_status fa_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v, const fa_view* o, const fa_view* dO,
