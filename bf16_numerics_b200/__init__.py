@@ -255,13 +255,16 @@ NO_WINDOW = 2**31 - 1
 def _call(device, stream, fn, *args):
     """fn(*args, stream handle) on `stream` (default: the device's current one) with `device` current."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        # (the handle alone: torch.cuda.current_stream builds a Stream around it, 2 us of a call's 10)
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    else:
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == device.index:
-        return fn(*args, stream.cuda_stream)
+        return fn(*args, handle)
     with torch.cuda.device(device):
-        return fn(*args, stream.cuda_stream)
+        return fn(*args, handle)
 
 
 def _device_of(q):
@@ -282,7 +285,7 @@ def _view(name, t, shape, device):
     s = t.stride()
     if s[3] != 1:
         raise ValueError(f"{name}: the last axis must be contiguous (strides {s})")
-    return ctypes.byref(_abi.FaView(t.data_ptr(), s[0], s[1], s[2]))
+    return _abi.FaView(t.data_ptr(), s[0], s[1], s[2])
 
 
 def _vec(name, t, shape, device, dtype=torch.float32):
@@ -301,7 +304,7 @@ def _window_stats(stats, rows, device):
     ptrs = [None if getattr(stats, n) is None else
             _vec(f"stats.{n}", getattr(stats, n), rows, device, torch.int32 if n == "rs" else torch.float32)
             for n in ("rm", "rs", "m", "pbar_max")]
-    return ctypes.byref(_abi.FaRowStats(*ptrs))
+    return _abi.FaRowStats(*ptrs)
 
 
 def fa_window_fwd(q, k, v, o, lse, stats: RowStats | None = None, window: int = NO_WINDOW, sinks: int = 0,
@@ -311,12 +314,18 @@ def fa_window_fwd(q, k, v, o, lse, stats: RowStats | None = None, window: int = 
     q, o [B, H, N, d] and k, v [B, Hkv, N, d] are bfloat16 tensors of any strides the header's ``fa_view`` allows
     (H a multiple of Hkv); lse and the statistics are contiguous [B, H, N]."""
     device = _device_of(q)
+    B, H, N, _ = q.shape
+    _window_fwd(device, q, k, v, _view("o", o, q.shape, device), _vec("lse", lse, (B, H, N), device),
+                _window_stats(stats, (B, H, N), device), window, sinks, softmax_mode, beta, stream)
+
+
+def _window_fwd(device, q, k, v, o, lse, stats, window, sinks, softmax_mode, beta, stream):
+    """fa_window_fwd for checked (or just allocated) outputs."""
     B, H, N, d = q.shape
     Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else -1
     kv = (B, Hkv, N, d)
     code = _call(device, stream, _abi.load().fa_window_fwd, _view("q", q, q.shape, device), _view("k", k, kv, device),
-                 _view("v", v, kv, device), _view("o", o, q.shape, device), _vec("lse", lse, (B, H, N), device),
-                 _window_stats(stats, (B, H, N), device), B, H, Hkv, N, d, window, sinks, softmax_mode, beta)
+                 _view("v", v, kv, device), o, lse, stats, B, H, Hkv, N, d, window, sinks, softmax_mode, beta)
     if code != _abi.FA_OK:
         raise FaError(code, "fa_window_fwd")
 
@@ -344,9 +353,12 @@ def fa_window_bwd(q, k, v, o, dO, lse, row_m, dq, dk, dv, workspace, window: int
         raise FaError(code, "fa_window_bwd")
 
 
-def _allocate_on(stream):
-    """Context in which new tensors belong to `stream` (None: the current one)."""
-    return torch.cuda.stream(stream)
+def _allocate(stream, make):
+    """make() with its new tensors belonging to `stream` (None: the current one)."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
 
 
 def window_attention_forward(q, k, v, window: int = NO_WINDOW, sinks: int = 0, softmax_mode: int = STABILIZED,
@@ -354,11 +366,18 @@ def window_attention_forward(q, k, v, window: int = NO_WINDOW, sinks: int = 0, s
     """Allocate outputs (torch; o strided like q) and run fa_window_fwd.  Returns (o, lse, stats)."""
     device = _device_of(q)
     B, H, N, _ = q.shape
-    with _allocate_on(stream):
-        o = torch.empty_like(q)
-        lse = torch.empty(B, H, N, device=device, dtype=torch.float32)
-        stats = RowStats.empty(B, H, N, device) if with_stats else None
-    fa_window_fwd(q, k, v, o, lse, stats, window, sinks, softmax_mode, beta, stream)
+    o, lse, rows = _allocate(stream, lambda: (
+        torch.empty_like(q), torch.empty(B, H, N, device=device, dtype=torch.float32),
+        torch.empty(4, B, H, N, device=device, dtype=torch.float32) if with_stats else None))
+    stats = ptrs = None
+    if with_stats:  # one allocation for the four
+        rm, rs, m, pbar_max = rows.unbind(0)
+        stats = RowStats(rm, rs.view(torch.int32), m, pbar_max)
+        at, step = rows.data_ptr(), 4 * lse.numel()
+        ptrs = _abi.FaRowStats(at, at + step, at + 2 * step, at + 3 * step)
+    so = o.stride()
+    _window_fwd(device, q, k, v, _abi.FaView(o.data_ptr(), so[0], so[1], so[2]), lse.data_ptr(), ptrs, window, sinks,
+                softmax_mode, beta, stream)
     return o, lse, stats
 
 
@@ -367,11 +386,10 @@ def window_attention_backward(q, k, v, o, dO, lse, row_m, window: int = NO_WINDO
     """Allocate gradients (torch; strided like q, k, v) and run fa_window_bwd.  Returns (dq, dk, dv, workspace)."""
     device = _device_of(q)
     B, H, N, d = q.shape
-    with _allocate_on(stream):
-        if workspace is None:
-            workspace = torch.empty(fa_window_bwd_workspace_bytes(B, H, k.shape[1], N, d, window, sinks),
-                                    device=device, dtype=torch.uint8)
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    size = 0 if workspace is not None else fa_window_bwd_workspace_bytes(B, H, k.shape[1], N, d, window, sinks)
+    dq, dk, dv, workspace = _allocate(stream, lambda: (
+        torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
+        torch.empty(size, device=device, dtype=torch.uint8) if workspace is None else workspace))
     fa_window_bwd(q, k, v, o, dO, lse, row_m, dq, dk, dv, workspace, window, sinks, softmax_mode, beta, stream)
     return dq, dk, dv, workspace
 
@@ -423,12 +441,10 @@ def cached_attention(q, k_pages, v_pages, page_table, ctx_len, tree=None, window
     Returns (o, lse)."""
     device = _device_of(q)
     B, H, T, d = q.shape
-    with _allocate_on(stream):
-        if workspace is None:
-            workspace = torch.empty(fa_cached_workspace_bytes(B, H, k_pages.shape[1], T, d), device=device,
-                                    dtype=torch.uint8)
-        o = torch.empty_like(q)
-        lse = torch.empty(B, H, T, device=device, dtype=torch.float32)
+    size = 0 if workspace is not None else fa_cached_workspace_bytes(B, H, k_pages.shape[1], T, d)
+    o, lse, workspace = _allocate(stream, lambda: (
+        torch.empty_like(q), torch.empty(B, H, T, device=device, dtype=torch.float32),
+        torch.empty(size, device=device, dtype=torch.uint8) if workspace is None else workspace))
     fa_cached_fwd(q, k_pages, v_pages, page_table, ctx_len, tree, o, lse, workspace, window, sinks, softmax_mode,
                   beta, stream)
     return o, lse
