@@ -422,14 +422,22 @@ def fa_cached_fwd(q, k_pages, v_pages, page_table, ctx_len, tree, o, lse, worksp
     tree: None (each new token sees itself and those before it) or int64 [B, T], the bits of word t naming the new
     tokens that token t sees.  page_table int32 [B, table_width], ctx_len int32 [B], workspace uint8."""
     device = _device_of(q)
+    B, H, T, _ = q.shape
+    _cached_fwd(device, q, k_pages, v_pages, page_table, ctx_len, tree, _view("o", o, q.shape, device),
+                _vec("lse", lse, (B, H, T), device), workspace, window, sinks, softmax_mode, beta, stream)
+
+
+def _cached_fwd(device, q, k_pages, v_pages, page_table, ctx_len, tree, o, lse, workspace, window, sinks, softmax_mode,
+                beta, stream):
+    """fa_cached_fwd for checked (or just allocated) outputs."""
     B, H, T, d = q.shape
     ptrs, sizes, tB, Hkv, td = _pool(k_pages, v_pages, page_table, ctx_len, device)
     if tB != B or td != d:
         raise ValueError(f"q is [{B}, {H}, {T}, {d}], the page table has {tB} rows and the pages rows of {td}")
+    size = workspace.numel()
     code = _call(device, stream, _abi.load().fa_cached_fwd, _view("q", q, q.shape, device), *ptrs,
-                 None if tree is None else _vec("tree", tree, (B, T), device, torch.int64),
-                 _view("o", o, q.shape, device), _vec("lse", lse, (B, H, T), device),
-                 _vec("workspace", workspace, (workspace.numel(),), device, torch.uint8), workspace.numel(),
+                 None if tree is None else _vec("tree", tree, (B, T), device, torch.int64), o, lse,
+                 _vec("workspace", workspace, (size,), device, torch.uint8), size,
                  B, H, Hkv, T, d, *sizes, window, sinks, softmax_mode, beta)
     if code != _abi.FA_OK:
         raise FaError(code, "fa_cached_fwd")
@@ -441,12 +449,13 @@ def cached_attention(q, k_pages, v_pages, page_table, ctx_len, tree=None, window
     Returns (o, lse)."""
     device = _device_of(q)
     B, H, T, d = q.shape
-    size = 0 if workspace is not None else fa_cached_workspace_bytes(B, H, k_pages.shape[1], T, d)
-    o, lse, workspace = _allocate(stream, lambda: (
-        torch.empty_like(q), torch.empty(B, H, T, device=device, dtype=torch.float32),
-        torch.empty(size, device=device, dtype=torch.uint8) if workspace is None else workspace))
-    fa_cached_fwd(q, k_pages, v_pages, page_table, ctx_len, tree, o, lse, workspace, window, sinks, softmax_mode,
-                  beta, stream)
+    if workspace is None:
+        size = fa_cached_workspace_bytes(B, H, k_pages.shape[1], T, d)
+        workspace = _allocate(stream, lambda: torch.empty(size, device=device, dtype=torch.uint8))
+    o, lse = _allocate(stream, lambda: (torch.empty_like(q), torch.empty(B, H, T, device=device, dtype=torch.float32)))
+    so = o.stride()
+    _cached_fwd(device, q, k_pages, v_pages, page_table, ctx_len, tree, _abi.FaView(o.data_ptr(), so[0], so[1], so[2]),
+                lse.data_ptr(), workspace, window, sinks, softmax_mode, beta, stream)
     return o, lse
 
 

@@ -4,10 +4,13 @@
 
 namespace {
 
-// How the T * G rows of a key head fill 128-row tiles: RT tiles of GT query
-// heads each (the last may hold fewer), C copies of a tile's R = GT * T rows.
+// How the T * G rows of a key head fill 128-row tiles: tiles of GT query heads
+// each (the last may hold fewer), C copies of a tile's R = GT * T rows; with more
+// than one tile (R is above 64 then) they are worked on in pairs.  RT: items, which
+// are tiles or pairs of them.
 struct CachedSplit {
   int GT, RT, R, C;
+  bool pair;
 };
 CachedSplit cached_split(int G, int T) {
   CachedSplit s{};
@@ -15,6 +18,8 @@ CachedSplit cached_split(int G, int T) {
   s.RT = (G + most - 1) / most;
   s.GT = (G + s.RT - 1) / s.RT;
   s.RT = (G + s.GT - 1) / s.GT;
+  s.pair = s.RT > 1;
+  if (s.pair) s.RT = (s.RT + 1) / 2;
   s.R = s.GT * T;
   s.C = s.R <= 32 ? 4 : (s.R <= 64 ? 2 : 1);
   return s;
@@ -23,13 +28,13 @@ CachedSplit cached_split(int G, int T) {
 constexpr int kCachedGrid = 160;  // most CTAs of the split kernel (one per SM)
 
 struct CachedLayoutBytes {
-  size_t prefix_off, ml_off, o_off, bytes;
+  size_t seg_off, ml_off, o_off, bytes;
 };
 CachedLayoutBytes cached_layout(int B, int Hkv, int d, const CachedSplit& s) {
   CachedLayoutBytes l{};
-  const size_t parts = (static_cast<size_t>(B) * Hkv * s.RT + kCachedGrid) * s.C * s.R;
-  l.prefix_off = 0;
-  l.ml_off = round256((static_cast<size_t>(B) + 1) * 8);
+  const size_t parts = (static_cast<size_t>(B) * Hkv * s.RT + kCachedGrid) * (s.pair ? 2 : s.C) * s.R;
+  l.seg_off = 0;
+  l.ml_off = round256(static_cast<size_t>(B) * Hkv * s.RT * 8);
   l.o_off = l.ml_off + round256(parts * 8);
   l.bytes = l.o_off + round256(parts * d * 4);
   return l;
@@ -42,7 +47,7 @@ fa_status cached_args(int B, int H, int Hkv, int T, int d, bool* empty) {
   *empty = static_cast<long long>(B) * H * T == 0;
   if (*empty) return FA_OK;
   if (Hkv == 0 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
-  if (T > 64) return FA_ERR_UNSUPPORTED;
+  if (T > 64 || static_cast<long long>(B) * H * T >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
@@ -78,19 +83,23 @@ bool make_map_pages(CUtensorMap* map, const void* ptr, int num_pages, int Hkv, i
   return encode_map_4d(map, ptr, dims, strides, box);
 }
 
-template <int D, int C>
+template <int D, int C, bool PAIR>
 fa_status launch_cached(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const fa::CachedParams& p,
-                        const fa::JoinParams& j, cudaStream_t stream) {
-  using L = fa::CachedLayout<D, C>;
+                        const fa::JoinParams& j, int grid, cudaStream_t stream) {
+  using L = fa::CachedLayout<D, C, PAIR>;
   static std::atomic<uint64_t> attr{0};
-  if (!ensure_smem(fa::fa_cached_kernel<D, C>, L::SMEM_BYTES, attr)) return FA_ERR_CUDA;
+  if (!ensure_smem(fa::fa_cached_kernel<D, C, PAIR>, L::SMEM_BYTES, attr)) return FA_ERR_CUDA;
   cudaError_t e;
-  e = launch_pdl(fa::fa_cached_kernel<D, C>, dim3(static_cast<unsigned>(j.grid)), dim3(L::THREADS), L::SMEM_BYTES,
+  e = launch_pdl(fa::fa_cached_kernel<D, C, PAIR>, dim3(static_cast<unsigned>(grid)), dim3(L::THREADS), L::SMEM_BYTES,
                  stream, mq, mk, mv, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail("fa_cached_kernel launch", e);
   const long long rows = static_cast<long long>(p.B) * p.H * p.T;
-  e = launch_pdl(fa::fa_cached_join_kernel<D, 4>, dim3(grid_for(rows, 1)), dim3(128), 0, stream, p, j);
+  // one warp per row once there are rows for every SM's warps, else eight
+  if (rows >= 16ll * grid)
+    e = launch_pdl(fa::fa_cached_join_kernel<D, 1>, dim3(grid_for(rows, 4)), dim3(128), 0, stream, p, j);
+  else
+    e = launch_pdl(fa::fa_cached_join_kernel<D, 8>, dim3(grid_for(rows, 1)), dim3(256), 0, stream, p, j);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? FA_OK : cuda_fail("fa_cached_join_kernel launch", e);
 }
@@ -100,8 +109,9 @@ fa_status run_cached(const fa_view* q, const void* k_pages, const void* v_pages,
                      fa::JoinParams j, const CachedSplit& s, cudaStream_t stream) {
   const int n_sm = sm_count();
   if (n_sm <= 0) return cuda_fail("cudaDeviceGetAttribute(multiprocessor count)");
-  j.grid = n_sm < kCachedGrid ? n_sm : kCachedGrid;
+  const int grid = n_sm < kCachedGrid ? n_sm : kCachedGrid;
   j.C = s.C;
+  j.pair = s.pair ? 1 : 0;
   j.so = strides_of(o);
   p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
   CUtensorMap mq, mk, mv;
@@ -116,9 +126,10 @@ fa_status run_cached(const fa_view* q, const void* k_pages, const void* v_pages,
   if (!make_map_pages(&mk, k_pages, p.num_pages, p.Hkv, p.page, D) ||
       !make_map_pages(&mv, v_pages, p.num_pages, p.Hkv, p.page, D))
     return cuda_fail("cuTensorMapEncodeTiled (pages)");
-  if (s.C == 4) return launch_cached<D, 4>(mq, mk, mv, p, j, stream);
-  if (s.C == 2) return launch_cached<D, 2>(mq, mk, mv, p, j, stream);
-  return launch_cached<D, 1>(mq, mk, mv, p, j, stream);
+  if (s.pair) return launch_cached<D, 1, true>(mq, mk, mv, p, j, grid, stream);
+  if (s.C == 4) return launch_cached<D, 4, false>(mq, mk, mv, p, j, grid, stream);
+  if (s.C == 2) return launch_cached<D, 2, false>(mq, mk, mv, p, j, grid, stream);
+  return launch_cached<D, 1, false>(mq, mk, mv, p, j, grid, stream);
 }
 
 fa::CachePool cache_pool(void* k_pages, void* v_pages, const int* table, const int* ctx_len, int Hkv, int num_pages,
@@ -159,7 +170,7 @@ fa_status fa_cached_fwd(const fa_view* q, const void* k_pages, const void* v_pag
   p.table = page_table;
   p.ctx_len = ctx_len;
   p.tree = reinterpret_cast<const unsigned long long*>(tree);
-  p.prefix = reinterpret_cast<long long*>(ws + l.prefix_off);
+  p.seg = reinterpret_cast<int*>(ws + l.seg_off);
   p.part_ml = reinterpret_cast<float2*>(ws + l.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + l.o_off);
   p.B = B;

@@ -338,6 +338,10 @@ namespace fa {
 __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
+// Arrive on it without waiting (whole warps; `count` includes their threads).
+__device__ __forceinline__ void named_barrier_arrive(uint32_t id, uint32_t count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
 // Named barrier that also ANDs a predicate over the participating threads:
 // every thread gets true only if every thread passed true.  Used where a group
 // of warps must take the same branch after a bounded wait (a wait that gave up
