@@ -298,6 +298,19 @@ def _vec(name, t, shape, device, dtype=torch.float32):
     return t.data_ptr()
 
 
+def _mask(window, sinks):
+    """The two as they are, once they fit the C ints they are passed as."""
+    if not (1 <= window <= NO_WINDOW and 0 <= sinks <= NO_WINDOW):
+        raise ValueError(f"window must be in [1, 2**31 - 1] and sinks in [0, 2**31 - 1], got {window} and {sinks}")
+    return window, sinks
+
+
+def _bytes(workspace, device):
+    """(data pointer, size) of a workspace."""
+    size = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+    return _vec("workspace", workspace, (size,), device, torch.uint8), size
+
+
 def _window_stats(stats, rows, device):
     if stats is None:
         return None
@@ -325,14 +338,14 @@ def _window_fwd(device, q, k, v, o, lse, stats, window, sinks, softmax_mode, bet
     Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else -1
     kv = (B, Hkv, N, d)
     code = _call(device, stream, _abi.load().fa_window_fwd, _view("q", q, q.shape, device), _view("k", k, kv, device),
-                 _view("v", v, kv, device), o, lse, stats, B, H, Hkv, N, d, window, sinks, softmax_mode, beta)
+                 _view("v", v, kv, device), o, lse, stats, B, H, Hkv, N, d, *_mask(window, sinks), softmax_mode, beta)
     if code != _abi.FA_OK:
         raise FaError(code, "fa_window_fwd")
 
 
 def fa_window_bwd_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int, window: int = NO_WINDOW,
                                   sinks: int = 0) -> int:
-    return int(_abi.load().fa_window_bwd_workspace_bytes(B, H, Hkv, N, d, window, sinks))
+    return int(_abi.load().fa_window_bwd_workspace_bytes(B, H, Hkv, N, d, *_mask(window, sinks)))
 
 
 def fa_window_bwd(q, k, v, o, dO, lse, row_m, dq, dk, dv, workspace, window: int = NO_WINDOW, sinks: int = 0,
@@ -347,8 +360,7 @@ def fa_window_bwd(q, k, v, o, dO, lse, row_m, dq, dk, dv, workspace, window: int
                  _vec("lse", lse, (B, H, N), device),
                  None if row_m is None else _vec("row_m", row_m, (B, H, N), device), _view("dq", dq, q.shape, device),
                  _view("dk", dk, kv, device), _view("dv", dv, kv, device),
-                 _vec("workspace", workspace, (workspace.numel(),), device, torch.uint8), workspace.numel(),
-                 B, H, Hkv, N, d, window, sinks, softmax_mode, beta)
+                 *_bytes(workspace, device), B, H, Hkv, N, d, *_mask(window, sinks), softmax_mode, beta)
     if code != _abi.FA_OK:
         raise FaError(code, "fa_window_bwd")
 
@@ -434,11 +446,9 @@ def _cached_fwd(device, q, k_pages, v_pages, page_table, ctx_len, tree, o, lse, 
     ptrs, sizes, tB, Hkv, td = _pool(k_pages, v_pages, page_table, ctx_len, device)
     if tB != B or td != d:
         raise ValueError(f"q is [{B}, {H}, {T}, {d}], the page table has {tB} rows and the pages rows of {td}")
-    size = workspace.numel()
     code = _call(device, stream, _abi.load().fa_cached_fwd, _view("q", q, q.shape, device), *ptrs,
                  None if tree is None else _vec("tree", tree, (B, T), device, torch.int64), o, lse,
-                 _vec("workspace", workspace, (size,), device, torch.uint8), size,
-                 B, H, Hkv, T, d, *sizes, window, sinks, softmax_mode, beta)
+                 *_bytes(workspace, device), B, H, Hkv, T, d, *sizes, *_mask(window, sinks), softmax_mode, beta)
     if code != _abi.FA_OK:
         raise FaError(code, "fa_cached_fwd")
 

@@ -33,8 +33,8 @@ FA_NUM_KERNELS = 4
 FA_ERRWORD_FWD = 1
 FA_ERRWORD_BWD_D64 = 3
 FA_ERRWORD_BWD_D128 = 4
-FA_ERRWORD_CACHED = 5
 FA_ERRWORD_CACHE_PAGE = 6
+FA_ERRWORD_CACHED = 7
 KERNEL_NAMES = ("fa_fwd_kernel", "fa_bwd_delta_kernel", "fa_bwd_main_kernel", "fa_bwd_dq_convert_kernel")
 
 # every symbol include/fa_b200.h declares

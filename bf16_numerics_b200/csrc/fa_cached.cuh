@@ -53,8 +53,8 @@
 
 namespace fa {
 
-constexpr uint32_t kErrCached = 5;  // error word ids: a wait ran out ...
-constexpr uint32_t kErrPage = 6;    // ... a page id, length or index outside the cache
+constexpr uint32_t kErrPage = 6;    // error word ids: a page id, length or index outside the cache ...
+constexpr uint32_t kErrCached = 7;  // ... a wait of the split kernel ran out
 
 __device__ __forceinline__ void report_page(uint32_t site, int b) {
   atomicCAS(&g_fa_error, 0u, (kErrPage << 24) | (site << 16) | (static_cast<uint32_t>(b) & 0xFFFFu));
@@ -215,6 +215,9 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       tma_prefetch_desc(&tm_v);
     }
     grid_dependency_wait();
+    // the pages may have been written by the grid before (fa_cache_append); the
+    // loads below read them through the async proxy
+    fence_proxy_async_all();
     const int HR = p.Hkv * p.RT;
     CachedTiles mine;  // sequence `lane` of the first 32
     mine.n = 0;
@@ -493,6 +496,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   int gp[2] = {0, 0};  // products finished per slot before this segment
   int g0 = 0;
   bool ok = true;
+  const bool stall = t == 0 && inject_stall_here(kErrCached);  // test hook (fa_debug_inject_stall)
   // Error discipline: all softmax warps meet on named barrier 1 at the end of
   // each segment, and (HS = 2) the two warpgroups of a slot on barrier 3 + t in
   // each tile, with AND votes.  A wait that gives up only clears `ok`; its warp
@@ -685,7 +689,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(bar(L::P_FULL + t));
+      if (!(stall && g0 + i == 0)) mbar_arrive(bar(L::P_FULL + t));
     }
     // ------------------------------------------------------- end of a segment
     // the two slots' states of lane r, joined, each warpgroup writing its part of
@@ -773,6 +777,7 @@ struct JoinParams {
   float* lse;  // [B, H, T]
   int C;        // parts of a row per segment
   int pair;     // 1: items are pairs of row tiles
+  int grid;     // CTAs of the split kernel
 };
 template <int D, int WPR>
 __global__ void __launch_bounds__(WPR > 4 ? 32 * WPR : 128)
@@ -799,7 +804,9 @@ fa_cached_join_kernel(const CachedParams p, const JoinParams q) {
     CachedTiles seq;
     seq.load(p, b);  // a sequence without tiles has no segments
     float m = -INFINITY, l = 0.f, acc[V] = {};
-    if (in && seq.n > 0) {
+    // (a split kernel that gave up on a wait leaves entries of the workspace as
+    // they were: what is no range of CTAs is not followed)
+    if (in && seq.n > 0 && cta.x >= 0 && cta.x <= cta.y && cta.y < q.grid) {
       const int parts = (cta.y - cta.x + 1) * q.C;
       // C copies of R rows per segment: part i of the row is at first + i R; a
       // pair of row tiles: at first + i 2 R

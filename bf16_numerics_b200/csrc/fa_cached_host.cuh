@@ -57,8 +57,8 @@ bool pool_ok(const void* k_pages, const void* v_pages, const int* table, const i
   if (num_pages < 1 || table_width < 1) return false;
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256) return false;
   if (static_cast<long long>(table_width) * page_size >= (1ll << 31)) return false;
-  // (the last factor apart: the first three stay below 2^62)
-  if (static_cast<long long>(num_pages) * page_size * d >= (1ll << 44) / (Hkv > 0 ? Hkv : 1)) return false;
+  // TMA: a page of all heads below 2^40 bytes; 16-byte indices of the pool below 2^63
+  if (static_cast<long long>(Hkv) * page_size * d >= (1ll << 39)) return false;
   if (!k_pages || !v_pages || !table || !ctx_len || !aligned16(k_pages) || !aligned16(v_pages)) return false;
   return !((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(ctx_len)) & 3u);
 }
@@ -112,6 +112,7 @@ fa_status run_cached(const fa_view* q, const void* k_pages, const void* v_pages,
   const int grid = n_sm < kCachedGrid ? n_sm : kCachedGrid;
   j.C = s.C;
   j.pair = s.pair ? 1 : 0;
+  j.grid = grid;
   j.so = strides_of(o);
   p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
   CUtensorMap mq, mk, mv;

@@ -555,7 +555,7 @@ fa_status fa_debug_set_wait_limit_ns(unsigned long long ns) {
 
 fa_status fa_debug_inject_stall(unsigned int kernel_id) {
   if (kernel_id != 0 && kernel_id != FA_ERRWORD_FWD && kernel_id != FA_ERRWORD_BWD_D64 &&
-      kernel_id != FA_ERRWORD_BWD_D128)
+      kernel_id != FA_ERRWORD_BWD_D128 && kernel_id != FA_ERRWORD_CACHED)
     return FA_ERR_INVALID_ARG;
   if (cudaMemcpyToSymbol(fa::g_fa_inject, &kernel_id, sizeof(kernel_id)) != cudaSuccess)
     return cuda_fail("cudaMemcpyToSymbol(stall injection)", cudaGetLastError());

@@ -168,9 +168,11 @@ fa_status fa_bwd_o_hp(const void* q, const void* k, const void* v, const float* 
  * fused projection are such views.  lse, row_m and the row statistics are
  * contiguous [B, H, N].
  *
- * Workspace, stream and errors are those of fa_fwd / fa_bwd.  dK and dV of a
- * call are reproducible unless the workspace query says otherwise below; dQ
- * sums fp32 partials in an order that varies (as in fa_bwd). */
+ * Workspace, stream and errors are those of fa_fwd / fa_bwd: the outputs o,
+ * lse, the statistics, dK and dV are reproducible; dQ sums fp32 partials in an
+ * order that varies (as in fa_bwd).  Like fa_bwd, fa_window_bwd takes lse and
+ * row_m from the forward with the same window, sinks, mode and beta.  K and V
+ * hold finite values (a hidden key's weight is 0, and 0 * inf is not). */
 typedef struct {
   void* ptr;
   long long stride_b, stride_h, stride_n;
@@ -180,7 +182,10 @@ fa_status fa_window_fwd(const fa_view* q, const fa_view* k, const fa_view* v, co
                         const fa_row_stats* stats, int B, int H, int Hkv, int N, int d, int window, int sinks,
                         int softmax_mode, float beta, void* stream);
 
-/* Bytes of workspace fa_window_bwd needs; 0 on bad sizes. */
+/* Bytes of workspace fa_window_bwd needs on the current device (the backward's
+ * work is cut up by the number of its multiprocessors); 0 on bad sizes.  The
+ * workspace holds delta, the fp32 dQ accumulator and the partial dK, dV of key
+ * blocks that are worked on in several pieces. */
 size_t fa_window_bwd_workspace_bytes(int B, int H, int Hkv, int N, int d, int window, int sinks);
 
 fa_status fa_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v, const fa_view* o, const fa_view* dO,
@@ -192,7 +197,7 @@ fa_status fa_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v, co
  * Attention over a paged key/value cache, and the cache's writes.
  *
  * The cache: k_pages and v_pages are bf16 pools [num_pages, Hkv, page_size, d],
- * contiguous and 16-byte aligned, page_size one of 16, 32, 64, 128, 256.  Row b of
+ * contiguous and 16-byte aligned (Hkv * page_size * d < 2^39), page_size one of 16, 32, 64, 128, 256.  Row b of
  * page_table (int32 [B, table_width]) names the pages of sequence b in order:
  * its slot j is row j % page_size of page page_table[b][j / page_size].
  * ctx_len (int32 [B]) is the number of tokens sequence b holds; slot j <
@@ -273,8 +278,8 @@ enum {
   FA_ERRWORD_FWD = 1,
   FA_ERRWORD_BWD_D64 = 3,
   FA_ERRWORD_BWD_D128 = 4,
-  FA_ERRWORD_CACHED = 5,
-  FA_ERRWORD_CACHE_PAGE = 6
+  FA_ERRWORD_CACHE_PAGE = 6,
+  FA_ERRWORD_CACHED = 7
 };
 fa_status fa_device_error(unsigned int* code);
 
@@ -289,9 +294,9 @@ fa_status fa_device_error(unsigned int* code);
  * (milliseconds) makes a withheld arrive end quickly; it must stay well above
  * the longest legitimate wait of the problem being run.
  *
- * fa_debug_inject_stall: kernel_id = FA_ERRWORD_FWD, _BWD_D64 or _BWD_D128
+ * fa_debug_inject_stall: kernel_id = FA_ERRWORD_FWD, _BWD_D64, _BWD_D128 or _CACHED
  * makes CTA 0 of every later launch of that kernel withhold its elementwise
- * warps' first arrive on the barrier that hands P_bar (forward) or P^T
+ * warps' first arrive on the barrier that hands P_bar (forward, cached) or P^T
  * (backward) to the MMA warp.  No bulk copy is outstanding on that barrier:
  * the MMA warp's wait runs out, the kernel records the error word, drains its
  * copies and products, frees its tensor memory and returns; fa_device_error
@@ -300,7 +305,8 @@ fa_status fa_device_error(unsigned int* code);
 fa_status fa_debug_set_wait_limit_ns(unsigned long long ns);
 fa_status fa_debug_inject_stall(unsigned int kernel_id);
 
-/* Per-kernel timing.  While enabled, every launch made by fa_fwd / fa_bwd is
+/* Per-kernel timing.  While enabled, every launch made by fa_fwd / fa_bwd and
+ * their windowed forms (under the same ids; not the calls on a cache) is
  * bracketed by two CUDA events recorded on the launching stream.
  * fa_timing_read synchronises on the recorded events, adds the elapsed times
  * per kernel id (FA_KERNEL_*), writes launch counts and total milliseconds

@@ -31,7 +31,7 @@ def attend(lib, kp=0x1000, vp=0x1000, table=0x1000, ctx=0x1000, tree=None, lse=0
 def test_attention_arguments(lib):
     for kw in (dict(window=0), dict(sinks=-1), dict(mode=5), dict(beta=1.0), dict(Hkv=3), dict(Hkv=0), dict(Hkv=8),
                dict(B=-1), dict(T=-1), dict(pages=0), dict(page=24), dict(page=0), dict(page=512), dict(width=0),
-               dict(width=1 << 27), dict(pages=1 << 30, page=256), dict(kp=None), dict(vp=0x1008), dict(table=None),
+               dict(width=1 << 27), dict(H=1 << 26, Hkv=1 << 25, T=1, B=1, page=256), dict(kp=None), dict(vp=0x1008), dict(table=None),
                dict(table=0x1002), dict(ctx=None), dict(ctx=0x1001), dict(tree=0x1004), dict(lse=None), dict(lse=0x1002),
                dict(q=view(2, 4, 3, 64, ptr=0)), dict(o=view(2, 4, 3, 64, strides=(0, 64, 256)))):
         assert attend(lib, **kw) == BAD, kw

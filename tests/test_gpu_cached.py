@@ -373,3 +373,26 @@ def test_prompt_then_tokens(cuda_device, d):
                 X.assert_within("lse", y[b], f["lse"], f["lse_bound"])
         at += T
         n += T
+
+
+@pytest.mark.parametrize("T,H,Hkv,d", [(1, 2, 1, 64), (9, 4, 1, 128), (64, 2, 1, 128), (48, 8, 1, 64)])
+def test_withheld_arrive_ends_in_timeout(cuda_device, T, H, Hkv, d):
+    """The bounded-wait exit of the split kernel in each of its forms (four, two and one copies of the rows, pairs of row
+    tiles): a hook withholds an arrive that nothing else gives, the call ends with FA_ERR_TIMEOUT, and the next
+    normal call on the same context is right."""
+    cache = Cache([900], T, Hkv, d, 64, seed=1)
+    q = _normal(torch.Generator(device="cuda").manual_seed(2), 1, H, T, d)
+    torch.cuda.synchronize()
+    assert fa.fa_device_error() == (0, 0)
+    try:
+        fa.fa_debug_set_wait_limit_ns(50_000_000)  # 50 ms: far above every legitimate wait here
+        fa.fa_debug_inject_stall(_abi.FA_ERRWORD_CACHED)
+        fa.cached_attention(q, cache.k, cache.v, cache.table, cache.ctx_len)
+        status, word = fa.fa_device_error()
+    finally:
+        fa.fa_debug_inject_stall(0)
+        fa.fa_debug_set_wait_limit_ns(0)
+    assert status == _abi.FA_ERR_TIMEOUT and word >> 24 == _abi.FA_ERRWORD_CACHED and word & 0xFFFF == 0
+    o, lse = fa.cached_attention(q, cache.k, cache.v, cache.table, cache.ctx_len)
+    assert fa.fa_device_error() == (0, 0)
+    _check(cache, q, _words("chain", 1, T, None), INF, 0, o, lse)

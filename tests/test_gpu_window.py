@@ -198,3 +198,31 @@ def test_streams_and_graph(cuda_device, d):
         for a, b in zip(got[:4], ref[:4]):
             assert torch.equal(a, b)
         assert (got[4].float() - ref[4].float()).abs().max() <= 2 * 2.0 ** -8 * ref[4].float().abs().max()
+
+
+def test_past_two_to_the_31_elements(cuda_device):
+    """Tensors of more than 2^31 elements: the last rows of the last head, whose window reaches only their neighbours,
+    against the formulas on a slice."""
+    H, Hkv, N, d, window = 10, 5, 1_700_000, 128, 100
+    assert H * N * d > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(4)
+    make = lambda h: torch.randn(1, h, N, d, device="cuda", generator=g, dtype=torch.bfloat16)
+    q, k, v, do = make(H), make(Hkv), make(Hkv), make(H)
+    o, lse, st = fa.window_attention_forward(q, k, v, window)
+    dq, dk, dv, ws = fa.window_attention_backward(q, k, v, o, do, lse, st.m, window)
+    assert fa.fa_device_error() == (0, 0)
+    n, m = 500, 300  # the last n rows hold the whole window of the last m
+    for h in (0, H - 1):
+        kv = h // 2
+        seen = X.visible(n, window, 0, "cuda")
+        sk = sv = bk = bv = 0
+        for hh in (2 * kv, 2 * kv + 1):
+            f = X.attention(q[0, hh, -n:], k[0, kv, -n:], v[0, kv, -n:], seen)
+            r = X.gradients(q[0, hh, -n:], k[0, kv, -n:], v[0, kv, -n:], o[0, hh, -n:], do[0, hh, -n:], f, f["lse_bound"])
+            sk, bk, sv, bv = sk + r["dk"], bk + r["dk_bound"], sv + r["dv"], bv + r["dv_bound"]
+            if hh == h:
+                X.assert_within("o", o[0, h, -m:], f["o"][-m:], X.rounded(f["o_bound"], f["o"])[-m:])
+                X.assert_within("lse", lse[0, h, -m:], f["lse"][-m:], f["lse_bound"][-m:])
+                X.assert_within("dq", dq[0, h, -m:], r["dq"][-m:], X.rounded(r["dq_bound"], r["dq"])[-m:])
+        X.assert_within("dk", dk[0, kv, -m:], sk[-m:], X.rounded(bk, sk)[-m:])
+        X.assert_within("dv", dv[0, kv, -m:], sv[-m:], X.rounded(bv, sv)[-m:])

@@ -76,3 +76,9 @@ def test_python_refuses_host_tensors():
         fa.window_attention_forward(x, x, x, 4)
     with pytest.raises(TypeError):
         fa.window_attention_forward(None, x, x, 4)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (-1, 0), (2**31, 0), (2**32 + 5, 0), (4, -1), (4, 2**31)])
+def test_python_refuses_masks_that_do_not_fit(window, sinks):
+    with pytest.raises(ValueError):
+        fa.fa_window_bwd_workspace_bytes(1, 2, 2, 100, 64, window, sinks)
