@@ -150,8 +150,9 @@ static_assert(FwdLayout<128, false>::o_col(1) + 128 <= 512 && FwdLayout<128, tru
 // tiles it does not see.  The diagonal tile comes first in each slot, so every
 // row has met a visible key before it meets a tile that hides all of its keys.
 struct FwdItemWindow {
-  // first window tile per slot, sink tiles of the launch, window tiles of the item, batch, heads
-  int lo[2], nsb, nwin, b, h, hk;
+  // window tiles of the item; the one step that slot 0 skips (the lowest window
+  // tile, where only slot 1's rows reach it; -1: none) and its last step; batch, heads
+  int nwin, skip, last0, b, h, hk;
 };
 struct FwdItemPlain {};
 template <int NT, bool WIN = false>
@@ -175,11 +176,13 @@ struct FwdItem : std::conditional_t<WIN, FwdItemWindow, FwdItemPlain> {
       this->b = bh / p.w.H;
       this->h = bh - this->b * p.w.H;
       this->hk = this->h / p.w.G;
-      this->nsb = p.w.n_sink_blk;
-      this->lo[0] = p.w.first_block(qblk[0]);
-      this->lo[1] = valid1 ? p.w.first_block(qblk[1]) : this->lo[0];
-      this->nwin = qblk[0] - this->lo[1] + 1;
-      nkv[0] = this->nwin + (this->nsb < this->lo[1] ? this->nsb : this->lo[1]);
+      // (neighbouring query blocks: their first window tiles differ by one at most)
+      const int nsb = p.w.n_sink_blk, lo0 = p.w.first_block(qblk[0]);
+      const int lo1 = valid1 ? p.w.first_block(qblk[1]) : lo0;
+      this->nwin = qblk[0] - lo1 + 1;
+      nkv[0] = nkv[1] = this->nwin + (nsb < lo1 ? nsb : lo1);
+      this->skip = lo1 < lo0 && lo1 >= nsb ? this->nwin - 1 : -1;
+      this->last0 = this->skip == nkv[0] - 1 ? nkv[0] - 2 : nkv[0] - 1;
       return true;
     }
     nkv[0] = p.causal ? qblk[0] + 1 : p.n_qblk;
@@ -196,8 +199,7 @@ struct FwdItem : std::conditional_t<WIN, FwdItemWindow, FwdItemPlain> {
   // whether slot t works on step j
   __device__ __forceinline__ bool active(int t, int j) const {
     if constexpr (WIN) {
-      const int kb = kblk(j);
-      return has(t) && j < nkv[0] && kb <= qblk[t] && (kb >= this->lo[t] || kb < this->nsb);
+      return j < nkv[0] && (t == 0 ? j != this->skip : valid1 && j > 0);
     } else {
       return has(t) && j < nkv[t];
     }
@@ -206,9 +208,8 @@ struct FwdItem : std::conditional_t<WIN, FwdItemWindow, FwdItemPlain> {
   __device__ __forceinline__ int first(int t) const { return WIN ? t : 0; }
   // whether j is slot t's last step (for an active one)
   __device__ __forceinline__ bool last(int t, int j) const {
-    // WIN: a slot can skip one tile between its window and its sinks
     if constexpr (WIN)
-      return !active(t, j + 1) && !active(t, j + 2);
+      return j == (t == 0 ? this->last0 : nkv[0] - 1);
     else
       return j + 1 >= nkv[t];
   }
