@@ -33,12 +33,14 @@ struct CachePool {
 
 // Token t of sequence b -> slot ctx_len[b] + t, for t < count[b] (null: all T).
 // Threads walk the 16-byte chunks of one sequence in (token, head, chunk)
-// order, U chunks of K and V each, all loads before any store.
+// order, U chunks of K and V each, all loads before any store.  Eight prompts of
+// up to 4096 tokens, 8 heads, d = 128 (207 MB in all): 39.5 us with U = 2 and at
+// most 8 blocks per SM, 41.5 us with U = 4 and 16, 47.9 us with U = 8.
 template <int D>
 __global__ void __launch_bounds__(256)
 fa_cache_append_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v, ViewStrides sk,
                        ViewStrides sv, const int* __restrict__ count, CachePool c, int B, int T) {
-  constexpr int CH = D / 8, U = 4;
+  constexpr int CH = D / 8, U = 2;
   grid_launch_dependents();
   grid_dependency_wait();
   for (int b = blockIdx.y; b < B; b += gridDim.y) {

@@ -207,10 +207,10 @@ fa_status fa_cache_append(const fa_view* k, const fa_view* v, void* k_pages, voi
       !view_ok(k, B, Hkv, T, d) || !view_ok(v, B, Hkv, T, d) || (reinterpret_cast<uintptr_t>(count) & 3u))
     return FA_ERR_INVALID_ARG;
   const fa::CachePool pool = cache_pool(k_pages, v_pages, page_table, ctx_len, Hkv, num_pages, page_size, table_width);
-  // blocks: one chunk of K and V per thread until 16 blocks per SM are there
+  // blocks: one chunk of K and V per thread until eight blocks per SM are there
   const long long work = static_cast<long long>(T) * Hkv * (d / 8);
   const int gy = B < 65535 ? B : 65535;
-  const long long most = (16ll * (sm_count() > 0 ? sm_count() : 148) + gy - 1) / gy;
+  const long long most = (8ll * (sm_count() > 0 ? sm_count() : 148) + gy - 1) / gy;
   long long gx = (work + 255) / 256;
   if (gx > most) gx = most;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
