@@ -275,27 +275,29 @@ def _device_of(q):
     return q.device
 
 
-def _view(name, t, shape, device):
-    """fa_view of a bf16 tensor of that shape on that device whose last axis is contiguous."""
+def _refuse(name, t, shape, device, dtype):
+    """Why `t` is no tensor of that shape, type and device, or not laid out as it has to be."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16 or t.device != device or t.shape != shape:
-        raise ValueError(f"{name} must be a bfloat16 tensor of shape {tuple(shape)} on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    s = t.stride()
-    if s[3] != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous (strides {s})")
-    return _abi.FaView(t.data_ptr(), s[0], s[1], s[2])
+    raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, contiguous (views: along "
+                     f"the last axis), got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+
+
+def _view(name, t, shape, device):
+    """fa_view of a bf16 tensor of that shape on that device whose last axis is contiguous."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape and t.device == device:
+        s = t.stride()
+        if s[3] == 1:
+            return _abi.FaView(t.data_ptr(), s[0], s[1], s[2])
+    _refuse(name, t, shape, device, torch.bfloat16)
 
 
 def _vec(name, t, shape, device, dtype=torch.float32):
     """data pointer of a contiguous tensor of that shape, type and device."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(name, t, shape, device, dtype)
 
 
 def _mask(window, sinks):
@@ -414,11 +416,12 @@ def _pool(k_pages, v_pages, page_table, ctx_len, device):
         raise ValueError("k_pages must be a bfloat16 tensor [num_pages, Hkv, page_size, d]")
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be an int32 tensor [B, table_width]")
-    P, Hkv, page, d = k_pages.shape
+    pages = k_pages.shape
+    P, Hkv, page, d = pages
     B, width = page_table.shape
-    ptrs = (_vec("k_pages", k_pages, (P, Hkv, page, d), device, torch.bfloat16),
-            _vec("v_pages", v_pages, (P, Hkv, page, d), device, torch.bfloat16),
-            _vec("page_table", page_table, (B, width), device, torch.int32),
+    ptrs = (_vec("k_pages", k_pages, pages, device, torch.bfloat16),
+            _vec("v_pages", v_pages, pages, device, torch.bfloat16),
+            _vec("page_table", page_table, page_table.shape, device, torch.int32),
             _vec("ctx_len", ctx_len, (B,), device, torch.int32))
     return ptrs, (P, page, width), B, Hkv, d
 
