@@ -64,8 +64,13 @@ struct CachedParams {
   const int* table;                  // [B, width] page ids
   const int* ctx_len;                // [B]
   const unsigned long long* tree;    // [B, T] or null: a chain
-  float* part_o;                     // [slots][C * R][D]: O against the slot's own shift
-  float2* part_ml;                   // [slots][C * R]: shift, sum
+  // partial results: O against the partial's own shift; shift and sum.  C > 1:
+  // [slots][C * R][D] and [slots][C * R].  Full row tiles: groups of eight rows, in runs of
+  // four columns -- [slots][tiles of an item][R8 / 8][D / 4][8][4] and
+  // [slots][tiles][R8], R8 = R rounded up to eights -- so that the rows of a warp fill
+  // whole lines (128 rows of 512 B a thread each took 4 us to write)
+  float* part_o;
+  float2* part_ml;
   int* seg;                          // [items][2]: the CTAs that hold an item's first and last tile
   int B, H, Hkv, T;
   int GT, RT, R;                     // heads per row tile, items per key head (row tiles or pairs), rows per row tile
@@ -511,7 +516,11 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       any = all_new;
     } else {
       const unsigned long long* words = p.tree + static_cast<long long>(cur.b) * p.T;
-      for (int u = 0; u < p.T; ++u) any |= __ldg(words + u);
+      const int lane = threadIdx.x & 31;
+      unsigned long long w = lane < p.T ? __ldg(words + lane) : 0ull;
+      if (lane + 32 < p.T) w |= __ldg(words + lane + 32);
+      any = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(w)) |
+            static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(w >> 32))) << 32;
       any &= all_new;
       bits = __ldg(words + tok) & all_new;
     }
@@ -704,15 +713,24 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     ok = named_barrier_and(1, L::SOFT, ok);
     if (!ok) break;
     tc_fence_after();
-    const long long at = cur.slot(p) * ((PAIR ? 2 : C) * p.R) + (PAIR ? t : copy) * p.R + (live ? row : 0);
+    constexpr int TILES = PAIR ? 2 : 1;
+    const int R8 = (p.R + 7) & ~7;
+    const long long at = C > 1 ? cur.slot(p) * (C * p.R) + copy * p.R + (live ? row : 0)
+                               : (cur.slot(p) * TILES + (PAIR ? t : 0)) * R8 + (live ? row : 0);
+    // full row tiles: where this row's first four columns go; four more: 8 float4 on
+    float4* dst8 = reinterpret_cast<float4*>(p.part_o) + (at & ~7ll) * (D / 4) + (at & 7);
     if constexpr (PAIR) {
       constexpr int CO = D / HS;  // columns per warpgroup
-      float* dst = p.part_o + at * D + h * CO;
 #pragma unroll 1
-      for (int c0 = 0; c0 < CO; c0 += 32) {
+      for (int c0 = h * CO; c0 < (h + 1) * CO; c0 += 32) {
         uint32_t a[32];
-        tmem_ld32(tmem + lane_base + L::o_col(t) + h * CO + c0, a);
-        if (live) store_part32(dst + c0, a, 1.f);
+        tmem_ld32(tmem + lane_base + L::o_col(t) + c0, a);
+        if (live) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            dst8[(c0 + c) * 2] = make_float4(__uint_as_float(a[c]), __uint_as_float(a[c + 1]),
+                                             __uint_as_float(a[c + 2]), __uint_as_float(a[c + 3]));
+        }
       }
       if (live && h == 0) p.part_ml[at] = make_float2(m_run, l + lds32(ml + 512 + (t * HS + 1) * 512));
     } else {
@@ -738,7 +756,10 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               v[e] = __uint_as_float(a[c + e]) * w0;
               if (n1 > 0) v[e] = fmaf(__uint_as_float(b[c + e]), w1, v[e]);
             }
-            *reinterpret_cast<float4*>(dst + c0 + c) = make_float4(v[0], v[1], v[2], v[3]);
+            if constexpr (C > 1)
+              *reinterpret_cast<float4*>(dst + c0 + c) = make_float4(v[0], v[1], v[2], v[3]);
+            else
+              dst8[(c_first + c0 + c) * 2] = make_float4(v[0], v[1], v[2], v[3]);
           }
         }
       }
@@ -765,7 +786,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   teardown();
 }
 
-// Joins the partial results of each row of the output.  A row's parts (segments
+// Joins the partial results of each row of the output (C > 1).  A row's parts (segments
 // x copies) are dealt to WPR warps; lane i of a warp holds its part i's shift and
 // sum, the weights come from shuffles, and the loads of the parts' O depend on
 // nothing but their addresses.  Bound by latency -- three loads, one after the
@@ -776,7 +797,6 @@ struct JoinParams {
   ViewStrides so;
   float* lse;  // [B, H, T]
   int C;        // parts of a row per segment
-  int pair;     // 1: items are pairs of row tiles
   int grid;     // CTAs of the split kernel
 };
 template <int D, int WPR>
@@ -797,8 +817,7 @@ fa_cached_join_kernel(const CachedParams p, const JoinParams q) {
     const bool in = id < rows;
     const int bh = (in ? id : 0) / p.T, tok = (in ? id : 0) - bh * p.T;
     const int b = bh / p.H, h = bh - b * p.H;
-    const int hk = h / G, g = h - hk * G, rt = g / p.GT;  // (rt: of all row tiles)
-    const int row = (g - rt * p.GT) * p.T + tok, hr = hk * p.RT + (rt >> q.pair);
+    const int hk = h / G, row = (h - hk * G) * p.T + tok, hr = hk;  // (few rows: one row tile)
     const long long item = static_cast<long long>(b) * HR + hr;
     const int2 cta = __ldcg(reinterpret_cast<const int2*>(p.seg) + item);
     CachedTiles seq;
@@ -808,10 +827,9 @@ fa_cached_join_kernel(const CachedParams p, const JoinParams q) {
     // they were: what is no range of CTAs is not followed)
     if (in && seq.n > 0 && cta.x >= 0 && cta.x <= cta.y && cta.y < q.grid) {
       const int parts = (cta.y - cta.x + 1) * q.C;
-      // C copies of R rows per segment: part i of the row is at first + i R; a
-      // pair of row tiles: at first + i 2 R
-      const int stride = p.R << q.pair;
-      const long long first = (item + cta.x) * (q.C * stride) + (rt & q.pair) * p.R + row;
+      // C copies of R rows per segment: part i of the row is at first + i R
+      const int stride = p.R;
+      const long long first = (item + cta.x) * (q.C * stride) + row;
       const int share = (parts + WPR - 1) / WPR, begin = sub * share;
       const int end = begin + share < parts ? begin + share : parts;
       for (int i0 = begin; i0 < end; i0 += 32) {
@@ -901,6 +919,101 @@ fa_cached_join_kernel(const CachedParams p, const JoinParams q) {
     else
       reinterpret_cast<uint32_t*>(dst)[lane] = pack_bf16x2(acc[0] * inv, acc[1] * inv);
     if (lane == 0) q.lse[id] = any ? m + logf(l) : -INFINITY;
+  }
+}
+
+// The same for full row tiles, whose partial results lie in groups of eight rows:
+// a warp takes a group (lane: row lane & 7, columns 4 (lane >> 3) + 16 k), so that
+// its loads are whole lines.  WPR warps share a group's segments.
+template <int D, int WPR>
+__global__ void __launch_bounds__(128)
+fa_cached_join_tiles_kernel(const CachedParams p, const JoinParams q, int tiles) {
+  constexpr int K = D / 16, GPB = 4 / WPR;
+  __shared__ float sh_m[4][8], sh_l[4][8];
+  __shared__ float sh_o[WPR > 1 ? 4 : 1][8][WPR > 1 ? D + 4 : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
+  const int r8 = lane & 7, cg = lane >> 3;
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int HR = p.Hkv * p.RT, G = p.H / p.Hkv, RG = (p.R + 7) / 8;
+  const long long groups = static_cast<long long>(p.B) * HR * tiles * RG;
+  for (long long g0 = static_cast<long long>(blockIdx.x) * GPB; g0 < groups; g0 += static_cast<long long>(gridDim.x) * GPB) {
+    const long long id = g0 + warp / WPR;
+    const bool in = id < groups;
+    const long long ti = (in ? id : 0) / RG, item = ti / tiles;  // (item, tile), item
+    const int rg = static_cast<int>((in ? id : 0) - ti * RG), tile = static_cast<int>(ti - item * tiles);
+    const int b = static_cast<int>(item / HR), hr = static_cast<int>(item - static_cast<long long>(b) * HR);
+    const int hk = hr / p.RT, rt = (hr - hk * p.RT) * tiles + tile;
+    const int row = rg * 8 + r8, g = rt * p.GT + row / p.T, tok = row % p.T;
+    const int2 cta = __ldcg(reinterpret_cast<const int2*>(p.seg) + item);
+    CachedTiles seq;
+    seq.load(p, b);
+    float m = -INFINITY, l = 0.f, acc[K][4] = {};
+    if (in && seq.n > 0 && cta.x >= 0 && cta.x <= cta.y && cta.y < q.grid) {
+      const int parts = cta.y - cta.x + 1, share = (parts + WPR - 1) / WPR;
+      const int begin = sub * share, end = begin + share < parts ? begin + share : parts;
+      for (int i = begin; i < end; ++i) {
+        const long long at = ((item + cta.x + i) * tiles + tile) * (RG * 8) + rg * 8;
+        // (rows past R of the last group hold nothing)
+        const float2 ml = row < p.R ? __ldcg(p.part_ml + at + r8) : make_float2(-INFINITY, 0.f);
+        const float4* src = reinterpret_cast<const float4*>(p.part_o) + at * (D / 4) + cg * 8 + r8;
+        float4 v[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = __ldcg(src + 32 * k);
+        if (ml.x > -INFINITY) {
+          const float mm = fmaxf(m, ml.x);
+          const float a = ex2_approx((m - mm) * kLog2e), w = ex2_approx((ml.x - mm) * kLog2e);
+          l = l * a + ml.y * w;
+          m = mm;
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            acc[k][0] = fmaf(v[k].x, w, acc[k][0] * a);
+            acc[k][1] = fmaf(v[k].y, w, acc[k][1] * a);
+            acc[k][2] = fmaf(v[k].z, w, acc[k][2] * a);
+            acc[k][3] = fmaf(v[k].w, w, acc[k][3] * a);
+          }
+        }
+      }
+    }
+    if constexpr (WPR > 1) {  // the warps' results, by the first
+      __syncthreads();
+      if (cg == 0) {
+        sh_m[warp][r8] = m;
+        sh_l[warp][r8] = l;
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        *reinterpret_cast<float4*>(&sh_o[warp][r8][16 * k + 4 * cg]) =
+            make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+      __syncthreads();
+      if (sub != 0) continue;
+#pragma unroll
+      for (int w = 1; w < WPR; ++w) {
+        const float mw = sh_m[warp + w][r8], mm = fmaxf(m, mw);
+        if (!(mw > -INFINITY)) continue;
+        const float a = ex2_approx((m - mm) * kLog2e), f = ex2_approx((mw - mm) * kLog2e);
+        l = l * a + sh_l[warp + w][r8] * f;
+        m = mm;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const float4 x = *reinterpret_cast<const float4*>(&sh_o[warp + w][r8][16 * k + 4 * cg]);
+          acc[k][0] = fmaf(x.x, f, acc[k][0] * a);
+          acc[k][1] = fmaf(x.y, f, acc[k][1] * a);
+          acc[k][2] = fmaf(x.z, f, acc[k][2] * a);
+          acc[k][3] = fmaf(x.w, f, acc[k][3] * a);
+        }
+      }
+    }
+    if (!in || row >= p.R || g >= G) continue;
+    const int h = hk * G + g;
+    const bool any = m > -INFINITY;
+    const float inv = any ? 1.f / l : 0.f;
+    __nv_bfloat16* dst = q.o + b * q.so.b + h * q.so.h + tok * q.so.n + 4 * cg;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      *reinterpret_cast<uint2*>(dst + 16 * k) =
+          make_uint2(pack_bf16x2(acc[k][0] * inv, acc[k][1] * inv), pack_bf16x2(acc[k][2] * inv, acc[k][3] * inv));
+    if (cg == 0) q.lse[(static_cast<long long>(b) * p.H + h) * p.T + tok] = any ? m + logf(l) : -INFINITY;
   }
 }
 

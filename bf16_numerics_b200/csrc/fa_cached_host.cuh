@@ -32,7 +32,9 @@ struct CachedLayoutBytes {
 };
 CachedLayoutBytes cached_layout(int B, int Hkv, int d, const CachedSplit& s) {
   CachedLayoutBytes l{};
-  const size_t parts = (static_cast<size_t>(B) * Hkv * s.RT + kCachedGrid) * (s.pair ? 2 : s.C) * s.R;
+  // rows per partial result: the copies', or the row tiles' in eights
+  const size_t rows = s.C > 1 ? static_cast<size_t>(s.C) * s.R : static_cast<size_t>(s.pair ? 2 : 1) * ((s.R + 7) & ~7);
+  const size_t parts = (static_cast<size_t>(B) * Hkv * s.RT + kCachedGrid) * rows;
   l.seg_off = 0;
   l.ml_off = round256(static_cast<size_t>(B) * Hkv * s.RT * 8);
   l.o_off = l.ml_off + round256(parts * 8);
@@ -94,6 +96,17 @@ fa_status launch_cached(const CUtensorMap& mq, const CUtensorMap& mk, const CUte
                  stream, mq, mk, mv, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail("fa_cached_kernel launch", e);
+  if constexpr (C == 1) {
+    // one warp per group of eight rows once there are some for every SM, else four
+    constexpr int tiles = PAIR ? 2 : 1;
+    const long long groups = static_cast<long long>(p.B) * p.Hkv * p.RT * tiles * ((p.R + 7) / 8);
+    if (groups >= 4ll * grid)
+      e = launch_pdl(fa::fa_cached_join_tiles_kernel<D, 1>, dim3(grid_for(groups, 4)), dim3(128), 0, stream, p, j, tiles);
+    else
+      e = launch_pdl(fa::fa_cached_join_tiles_kernel<D, 4>, dim3(grid_for(groups, 1)), dim3(128), 0, stream, p, j, tiles);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? FA_OK : cuda_fail("fa_cached_join_tiles_kernel launch", e);
+  }
   const long long rows = static_cast<long long>(p.B) * p.H * p.T;
   // one warp per row once there are rows for every SM's warps, else eight
   if (rows >= 16ll * grid)
@@ -111,7 +124,6 @@ fa_status run_cached(const fa_view* q, const void* k_pages, const void* v_pages,
   if (n_sm <= 0) return cuda_fail("cudaDeviceGetAttribute(multiprocessor count)");
   const int grid = n_sm < kCachedGrid ? n_sm : kCachedGrid;
   j.C = s.C;
-  j.pair = s.pair ? 1 : 0;
   j.grid = grid;
   j.so = strides_of(o);
   p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
