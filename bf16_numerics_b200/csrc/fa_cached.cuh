@@ -526,8 +526,9 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     const bool absent = bits == 0ull;  // works like a row that sees the context; its result is put down as empty
     lo = ctx + __popcll(bits) - p.window;  // first key of the window (pos - window + 1)
-    if (p.window < p.T && !absent) {
-      // some new tokens may be out of the window too
+    if (p.window <= p.T && !absent) {
+      // some new tokens may be out of the window too (positions of new tokens are
+      // in [ctx - 1, ctx + T): an absent one's is ctx - 1)
       const int pos = ctx + __popcll(bits) - 1;
       unsigned long long keep = 0ull;
       for (int u = 0; u < p.T; ++u) {

@@ -217,7 +217,7 @@ fa_status fa_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v, co
  *   slot j < ctx_len[b]  if  pos(t) - j < window or j < sinks,
  *   new token u          if  its bit is set and (pos(t) - pos(u) < window or pos(u) < sinks).
  * A token whose word is zero is absent: o = 0 and lse = -inf in its row, and its
- * slot need not have been written.  window >= 1 (2^31 - 1: no window), sinks
+ * slot need not have been written unless another token's word names it.  window >= 1 (2^31 - 1: no window), sinks
  * >= 0.  Softmax modes as in fa_fwd; the context is processed in parts that are
  * joined at the end, and the shift rule applies to the keys of each part.
  * With tied maxima the rule moves the shift by |rm| (beta - 1) or |rm|: as in

@@ -141,6 +141,14 @@ def test_windows_and_trees(cuda_device, d, window, sinks, kind):
     _run([0, 3, 200, 640, 1111], 11, 4, 2, d, 32, window, sinks, kind, seed=window % 1000 + sinks % 1000)
 
 
+@pytest.mark.parametrize("T", [2, 3, 7])
+def test_window_as_long_as_the_tree(cuda_device, T):
+    """A token may name an absent one, which stands one place before the root: T places away at most."""
+    for window in (T - 1, T, T + 1):
+        for seed in range(4):
+            _run([176, 28, 90, 5, 0], T, 4, 2, 64, 32, window, seed % 3, "absent", seed=seed)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_long_context_is_split_and_joined(cuda_device, d):
     _run([40000], 1, 2, 1, d, 128, seed=1)
