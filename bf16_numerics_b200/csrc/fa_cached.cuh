@@ -38,10 +38,16 @@
 // slot has two warpgroups, which halve the columns of each row and exchange
 // maxima and tie counts through shared memory.  Where a key head has more than
 // 128 rows (PAIR) the slots hold two row tiles instead and both take every tile:
-// K and V cross from L2 to the SM once for 256 rows (4 x 64 tokens, 32 heads over
-// 4, contexts to 32768, d = 128: 135 us with a row tile at a time, 131 us so).  One warp loads (TMA: K and V
-// through rings, one box per page, so a page may lie anywhere and be smaller
-// than a tile), one issues products.
+// K and V cross from L2 to the SM once for 256 rows (4 sequences of 64 tokens, 32
+// heads over 4, contexts to 32768, d = 128: 135 us with a row tile at a time, 131
+// us so).  One warp loads (TMA: K and V through rings, one box per page, so a page
+// may lie anywhere and be smaller than a tile), one issues products.
+//
+// Measured there: a row tile's step takes ~3600 cycles where its products need
+// 1024 -- scores from TMEM, maximum and ties 950, exponentials 1500, P_bar and the
+// rescale of O 700-950, then P V and the next S 1400 in the issuing thread, one
+// after the other.  With few rows the loads bind: 64 sequences to 8192, 16 heads
+// over 4, d = 128 (675 MB): 119 us, of which 105 at 6.4 TB/s.
 //   TMEM: S_t [128t, 128t+128), P_bar_t over its first 64 columns, O_t at 256 + D t.
 // Pages that no row sees are not read (their place is filled with zeros by an
 // out-of-range box); what lies in a read page behind the last token, or in the
