@@ -3,7 +3,8 @@
 Thin marshalling layer over the C ABI of ``libfa_b200.so`` (include/fa_b200.h).
 Every function with an ``fa_`` name maps 1:1 to the C entry point of the same
 name; tensors are passed as device pointers, the stream as the CUDA stream
-handle.  PyTorch only provides device memory and streams.  There is no CPU or
+handle.  The windowed and the cached calls, which a model makes per layer and
+token, are marshalled in C++ (csrc/fa_torch.cpp), the others with ctypes.  PyTorch only provides device memory and streams.  There is no CPU or
 library fallback: if the CUDA library is missing, importing the entry points
 raises.
 
@@ -252,74 +253,21 @@ def attention_backward(q, k, v, o, dO, lse, row_m, causal: bool = True, softmax_
 NO_WINDOW = 2**31 - 1
 
 
-def _call(device, stream, fn, *args):
-    """fn(*args, stream handle) on `stream` (default: the device's current one) with `device` current."""
+def _call(stream, device_of, name, *args):
+    """The library call ``name`` through the C++ marshalling (csrc/fa_torch.cpp): on the current stream of the tensors'
+    device, or on ``stream``, to which new tensors then belong."""
+    call = getattr(_abi.marshal(), name)
     if stream is None:
-        # (the handle alone: torch.cuda.current_stream builds a Stream around it, 2 us of a call's 10)
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    else:
-        handle = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
-        return fn(*args, handle)
-    with torch.cuda.device(device):
-        return fn(*args, handle)
+        return call(*args)
+    if stream.device != device_of.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device_of.device}")
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
-def _device_of(q):
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    if q.dim() != 4 or not q.is_cuda:
-        raise ValueError("q must be a CUDA bfloat16 tensor [B, H, N, d]")
-    return q.device
-
-
-def _refuse(name, t, shape, device, dtype):
-    """Why `t` is no tensor of that shape, type and device, or not laid out as it has to be."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}, contiguous (views: along "
-                     f"the last axis), got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
-
-
-def _view(name, t, shape, device):
-    """fa_view of a bf16 tensor of that shape on that device whose last axis is contiguous."""
-    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape and t.device == device:
-        s = t.stride()
-        if s[3] == 1:
-            return _abi.FaView(t.data_ptr(), s[0], s[1], s[2])
-    _refuse(name, t, shape, device, torch.bfloat16)
-
-
-def _vec(name, t, shape, device, dtype=torch.float32):
-    """data pointer of a contiguous tensor of that shape, type and device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
-            and t.is_contiguous()):
-        return t.data_ptr()
-    _refuse(name, t, shape, device, dtype)
-
-
-def _mask(window, sinks):
-    """The two as they are, once they fit the C ints they are passed as."""
-    if not (1 <= window <= NO_WINDOW and 0 <= sinks <= NO_WINDOW):
-        raise ValueError(f"window must be in [1, 2**31 - 1] and sinks in [0, 2**31 - 1], got {window} and {sinks}")
-    return window, sinks
-
-
-def _bytes(workspace, device):
-    """(data pointer, size) of a workspace."""
-    size = workspace.numel() if isinstance(workspace, torch.Tensor) else 0
-    return _vec("workspace", workspace, (size,), device, torch.uint8), size
-
-
-def _window_stats(stats, rows, device):
-    if stats is None:
-        return None
-    ptrs = [None if getattr(stats, n) is None else
-            _vec(f"stats.{n}", getattr(stats, n), rows, device, torch.int32 if n == "rs" else torch.float32)
-            for n in ("rm", "rs", "m", "pbar_max")]
-    return _abi.FaRowStats(*ptrs)
+def _checked(code, what):
+    if code != _abi.FA_OK:
+        raise FaError(code, what)
 
 
 def fa_window_fwd(q, k, v, o, lse, stats: RowStats | None = None, window: int = NO_WINDOW, sinks: int = 0,
@@ -328,103 +276,44 @@ def fa_window_fwd(q, k, v, o, lse, stats: RowStats | None = None, window: int = 
 
     q, o [B, H, N, d] and k, v [B, Hkv, N, d] are bfloat16 tensors of any strides the header's ``fa_view`` allows
     (H a multiple of Hkv); lse and the statistics are contiguous [B, H, N]."""
-    device = _device_of(q)
-    B, H, N, _ = q.shape
-    _window_fwd(device, q, k, v, _view("o", o, q.shape, device), _vec("lse", lse, (B, H, N), device),
-                _window_stats(stats, (B, H, N), device), window, sinks, softmax_mode, beta, stream)
-
-
-def _window_fwd(device, q, k, v, o, lse, stats, window, sinks, softmax_mode, beta, stream):
-    """fa_window_fwd for checked (or just allocated) outputs."""
-    B, H, N, d = q.shape
-    Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else -1
-    kv = (B, Hkv, N, d)
-    code = _call(device, stream, _abi.load().fa_window_fwd, _view("q", q, q.shape, device), _view("k", k, kv, device),
-                 _view("v", v, kv, device), o, lse, stats, B, H, Hkv, N, d, *_mask(window, sinks), softmax_mode, beta)
-    if code != _abi.FA_OK:
-        raise FaError(code, "fa_window_fwd")
+    rows = (None,) * 4 if stats is None else (stats.rm, stats.rs, stats.m, stats.pbar_max)
+    _checked(_call(stream, q, "window_fwd", q, k, v, o, lse, *rows, window, sinks, softmax_mode, beta),
+             "fa_window_fwd")
 
 
 def fa_window_bwd_workspace_bytes(B: int, H: int, Hkv: int, N: int, d: int, window: int = NO_WINDOW,
                                   sinks: int = 0) -> int:
-    return int(_abi.load().fa_window_bwd_workspace_bytes(B, H, Hkv, N, d, *_mask(window, sinks)))
+    if not (1 <= window <= NO_WINDOW and 0 <= sinks <= NO_WINDOW):
+        raise ValueError(f"window must be in [1, 2**31 - 1] and sinks in [0, 2**31 - 1], got {window} and {sinks}")
+    return int(_abi.load().fa_window_bwd_workspace_bytes(B, H, Hkv, N, d, window, sinks))
 
 
 def fa_window_bwd(q, k, v, o, dO, lse, row_m, dq, dk, dv, workspace, window: int = NO_WINDOW, sinks: int = 0,
                   softmax_mode: int = STABILIZED, beta: float = 2.0, stream=None) -> None:
     """C ``fa_window_bwd``: writes dq [B, H, N, d], dk and dv [B, Hkv, N, d]; workspace is a uint8 CUDA tensor."""
-    device = _device_of(q)
-    B, H, N, d = q.shape
-    Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else -1
-    kv = (B, Hkv, N, d)
-    code = _call(device, stream, _abi.load().fa_window_bwd, _view("q", q, q.shape, device), _view("k", k, kv, device),
-                 _view("v", v, kv, device), _view("o", o, q.shape, device), _view("dO", dO, q.shape, device),
-                 _vec("lse", lse, (B, H, N), device),
-                 None if row_m is None else _vec("row_m", row_m, (B, H, N), device), _view("dq", dq, q.shape, device),
-                 _view("dk", dk, kv, device), _view("dv", dv, kv, device),
-                 *_bytes(workspace, device), B, H, Hkv, N, d, *_mask(window, sinks), softmax_mode, beta)
-    if code != _abi.FA_OK:
-        raise FaError(code, "fa_window_bwd")
-
-
-def _allocate(stream, make):
-    """make() with its new tensors belonging to `stream` (None: the current one)."""
-    if stream is None:
-        return make()
-    with torch.cuda.stream(stream):
-        return make()
+    _checked(_call(stream, q, "window_bwd", q, k, v, o, dO, lse, row_m, dq, dk, dv, workspace, window, sinks,
+                      softmax_mode, beta), "fa_window_bwd")
 
 
 def window_attention_forward(q, k, v, window: int = NO_WINDOW, sinks: int = 0, softmax_mode: int = STABILIZED,
                              beta: float = 2.0, with_stats: bool = True, stream=None):
     """Allocate outputs (torch; o strided like q) and run fa_window_fwd.  Returns (o, lse, stats)."""
-    device = _device_of(q)
-    B, H, N, _ = q.shape
-    o, lse, rows = _allocate(stream, lambda: (
-        torch.empty_like(q), torch.empty(B, H, N, device=device, dtype=torch.float32),
-        torch.empty(4, B, H, N, device=device, dtype=torch.float32) if with_stats else None))
-    stats = ptrs = None
-    if with_stats:  # one allocation for the four
-        rm, rs, m, pbar_max = rows.unbind(0)
-        stats = RowStats(rm, rs.view(torch.int32), m, pbar_max)
-        at, step = rows.data_ptr(), 4 * lse.numel()
-        ptrs = _abi.FaRowStats(at, at + step, at + 2 * step, at + 3 * step)
-    so = o.stride()
-    _window_fwd(device, q, k, v, _abi.FaView(o.data_ptr(), so[0], so[1], so[2]), lse.data_ptr(), ptrs, window, sinks,
-                softmax_mode, beta, stream)
-    return o, lse, stats
+    code, o, lse, *rows = _call(stream, q, "window_forward", q, k, v, window, sinks, softmax_mode, beta,
+                                   bool(with_stats))
+    _checked(code, "fa_window_fwd")
+    return o, lse, RowStats(*rows) if rows else None
 
 
 def window_attention_backward(q, k, v, o, dO, lse, row_m, window: int = NO_WINDOW, sinks: int = 0,
                               softmax_mode: int = STABILIZED, beta: float = 2.0, workspace=None, stream=None):
     """Allocate gradients (torch; strided like q, k, v) and run fa_window_bwd.  Returns (dq, dk, dv, workspace)."""
-    device = _device_of(q)
-    B, H, N, d = q.shape
-    size = 0 if workspace is not None else fa_window_bwd_workspace_bytes(B, H, k.shape[1], N, d, window, sinks)
-    dq, dk, dv, workspace = _allocate(stream, lambda: (
-        torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
-        torch.empty(size, device=device, dtype=torch.uint8) if workspace is None else workspace))
-    fa_window_bwd(q, k, v, o, dO, lse, row_m, dq, dk, dv, workspace, window, sinks, softmax_mode, beta, stream)
-    return dq, dk, dv, workspace
+    code, *out = _call(stream, q, "window_backward", q, k, v, o, dO, lse, row_m, workspace, window, sinks,
+                          softmax_mode, beta)
+    _checked(code, "fa_window_bwd")
+    return tuple(out)
 
 
 # ------------------------------------------------------------- a paged cache
-
-def _pool(k_pages, v_pages, page_table, ctx_len, device):
-    """(pointers, (num_pages, page_size, table_width), B, Hkv, d) of a cache."""
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
-        raise ValueError("k_pages must be a bfloat16 tensor [num_pages, Hkv, page_size, d]")
-    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-        raise ValueError("page_table must be an int32 tensor [B, table_width]")
-    pages = k_pages.shape
-    P, Hkv, page, d = pages
-    B, width = page_table.shape
-    ptrs = (_vec("k_pages", k_pages, pages, device, torch.bfloat16),
-            _vec("v_pages", v_pages, pages, device, torch.bfloat16),
-            _vec("page_table", page_table, page_table.shape, device, torch.int32),
-            _vec("ctx_len", ctx_len, (B,), device, torch.int32))
-    return ptrs, (P, page, width), B, Hkv, d
-
 
 def fa_cached_workspace_bytes(B: int, H: int, Hkv: int, T: int, d: int) -> int:
     return int(_abi.load().fa_cached_workspace_bytes(B, H, Hkv, T, d))
@@ -436,62 +325,26 @@ def fa_cached_fwd(q, k_pages, v_pages, page_table, ctx_len, tree, o, lse, worksp
 
     tree: None (each new token sees itself and those before it) or int64 [B, T], the bits of word t naming the new
     tokens that token t sees.  page_table int32 [B, table_width], ctx_len int32 [B], workspace uint8."""
-    device = _device_of(q)
-    B, H, T, _ = q.shape
-    _cached_fwd(device, q, k_pages, v_pages, page_table, ctx_len, tree, _view("o", o, q.shape, device),
-                _vec("lse", lse, (B, H, T), device), workspace, window, sinks, softmax_mode, beta, stream)
-
-
-def _cached_fwd(device, q, k_pages, v_pages, page_table, ctx_len, tree, o, lse, workspace, window, sinks, softmax_mode,
-                beta, stream):
-    """fa_cached_fwd for checked (or just allocated) outputs."""
-    B, H, T, d = q.shape
-    ptrs, sizes, tB, Hkv, td = _pool(k_pages, v_pages, page_table, ctx_len, device)
-    if tB != B or td != d:
-        raise ValueError(f"q is [{B}, {H}, {T}, {d}], the page table has {tB} rows and the pages rows of {td}")
-    code = _call(device, stream, _abi.load().fa_cached_fwd, _view("q", q, q.shape, device), *ptrs,
-                 None if tree is None else _vec("tree", tree, (B, T), device, torch.int64), o, lse,
-                 *_bytes(workspace, device), B, H, Hkv, T, d, *sizes, *_mask(window, sinks), softmax_mode, beta)
-    if code != _abi.FA_OK:
-        raise FaError(code, "fa_cached_fwd")
+    _checked(_call(stream, q, "cached_fwd", q, k_pages, v_pages, page_table, ctx_len, tree, o, lse, workspace, window,
+                      sinks, softmax_mode, beta), "fa_cached_fwd")
 
 
 def cached_attention(q, k_pages, v_pages, page_table, ctx_len, tree=None, window: int = NO_WINDOW, sinks: int = 0,
                      softmax_mode: int = STABILIZED, beta: float = 2.0, workspace=None, stream=None):
     """Allocate outputs (torch; o strided like q), and a workspace if none is given, and run fa_cached_fwd.
     Returns (o, lse)."""
-    device = _device_of(q)
-    B, H, T, d = q.shape
-    if workspace is None:
-        size = fa_cached_workspace_bytes(B, H, k_pages.shape[1], T, d)
-        workspace = _allocate(stream, lambda: torch.empty(size, device=device, dtype=torch.uint8))
-    o, lse = _allocate(stream, lambda: (torch.empty_like(q), torch.empty(B, H, T, device=device, dtype=torch.float32)))
-    so = o.stride()
-    _cached_fwd(device, q, k_pages, v_pages, page_table, ctx_len, tree, _abi.FaView(o.data_ptr(), so[0], so[1], so[2]),
-                lse.data_ptr(), workspace, window, sinks, softmax_mode, beta, stream)
+    code, o, lse = _call(stream, q, "cached", q, k_pages, v_pages, page_table, ctx_len, tree, workspace, window, sinks,
+                            softmax_mode, beta)
+    _checked(code, "fa_cached_fwd")
     return o, lse
 
 
 def fa_cache_append(k, v, k_pages, v_pages, page_table, ctx_len, count=None, stream=None) -> None:
     """C ``fa_cache_append``: row t of k, v [B, Hkv, T, d] into slot ctx_len[b] + t, for t < count[b] (None: all)."""
-    device = _device_of(k)
-    B, Hkv, T, d = k.shape
-    ptrs, sizes, tB, pH, td = _pool(k_pages, v_pages, page_table, ctx_len, device)
-    if (tB, pH, td) != (B, Hkv, d):
-        raise ValueError(f"k is [{B}, {Hkv}, {T}, {d}], the cache has {tB} sequences, {pH} heads and rows of {td}")
-    code = _call(device, stream, _abi.load().fa_cache_append, _view("k", k, k.shape, device),
-                 _view("v", v, k.shape, device), *ptrs,
-                 None if count is None else _vec("count", count, (B,), device, torch.int32), B, Hkv, T, d, *sizes)
-    if code != _abi.FA_OK:
-        raise FaError(code, "fa_cache_append")
+    _checked(_call(stream, k, "append", k, v, k_pages, v_pages, page_table, ctx_len, count), "fa_cache_append")
 
 
 def fa_cache_compact(k_pages, v_pages, page_table, ctx_len, src, count, stream=None) -> None:
     """C ``fa_cache_compact``: slot ctx_len[b] + i takes the row of slot ctx_len[b] + src[b, i], for i < count[b]."""
-    device = _device_of(k_pages)
-    ptrs, sizes, B, Hkv, d = _pool(k_pages, v_pages, page_table, ctx_len, device)
-    M = src.shape[1] if isinstance(src, torch.Tensor) and src.dim() == 2 else -1
-    code = _call(device, stream, _abi.load().fa_cache_compact, *ptrs, _vec("src", src, (B, M), device, torch.int32),
-                 _vec("count", count, (B,), device, torch.int32), B, Hkv, M, d, *sizes)
-    if code != _abi.FA_OK:
-        raise FaError(code, "fa_cache_compact")
+    _checked(_call(stream, k_pages, "compact", k_pages, v_pages, page_table, ctx_len, src, count),
+             "fa_cache_compact")

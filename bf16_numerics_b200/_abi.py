@@ -111,5 +111,23 @@ def load() -> ctypes.CDLL:
     return lib
 
 
+#: entry points that csrc/fa_torch.cpp calls, in its order
+MARSHALLED = ("fa_window_fwd", "fa_window_bwd", "fa_window_bwd_workspace_bytes", "fa_cached_fwd",
+              "fa_cached_workspace_bytes", "fa_cache_append", "fa_cache_compact")
+_bound = None
+
+
+def marshal():
+    """The C++ marshalling module, bound to the loaded library."""
+    global _bound
+    if _bound is None:
+        lib = load()
+        from . import _marshal
+
+        _marshal.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in MARSHALLED))
+        _bound = _marshal
+    return _bound
+
+
 def status_string(code: int) -> str:
     return load().fa_status_string(code).decode()

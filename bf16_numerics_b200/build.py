@@ -4,7 +4,8 @@
 
 The library is a single translation unit (csrc/fa_lib.cu) that includes the
 kernel headers; the CUDA runtime is linked statically so the library does not
-depend on the runtime version PyTorch ships.
+depend on the runtime version PyTorch ships.  _marshal.so (csrc/fa_torch.cpp,
+g++) turns torch tensors into calls of the library.
 """
 
 from __future__ import annotations
@@ -24,6 +25,25 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(
     os.path.join(INCLUDE, "fa_b200.h")]
 
 
+MARSHAL_PATH = os.path.join(PKG_DIR, "_marshal.so")
+MARSHAL_SOURCE = os.path.join(CSRC, "fa_torch.cpp")
+
+
+def marshal_command(out: str = MARSHAL_PATH) -> list[str]:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import CUDA_HOME, include_paths, library_paths
+
+    libs = library_paths()
+    cuda = os.path.join(CUDA_HOME or os.path.dirname(os.path.dirname(nvcc_path())), "include")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+            *(f"-I{d}" for d in include_paths()), f"-I{cuda}", f"-I{sysconfig.get_paths()['include']}", MARSHAL_SOURCE,
+            "-o", out, *(f"-L{d}" for d in libs), *(f"-Wl,-rpath,{d}" for d in libs), "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python"]
+
+
 def nvcc_path() -> str:
     cand = os.environ.get("NVCC") or shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
     if not os.path.exists(cand):
@@ -36,25 +56,29 @@ def nvcc_command(out: str = LIB_PATH, extra=()) -> list[str]:
             "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", f"-I{INCLUDE}", *extra, "-o", out, *SOURCES]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+def up_to_date(out: str = LIB_PATH, deps=DEPS) -> bool:
+    if not os.path.exists(out):
         return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(p) <= t for p in DEPS)
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(p) <= t for p in deps)
 
 
-def build_library(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB_PATH
-    cmd = nvcc_command(extra=("-Xptxas", "-v") if verbose else ())
-    tmp = LIB_PATH + ".tmp"
-    cmd[cmd.index(LIB_PATH)] = tmp
+def _compile(cmd: list[str], out: str, verbose: bool) -> None:
+    tmp = out + ".tmp"
+    cmd = [tmp if arg == out else arg for arg in cmd]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if verbose or res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
     if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed with exit code {res.returncode}")
-    os.replace(tmp, LIB_PATH)
+        raise RuntimeError(f"{cmd[0]} failed with exit code {res.returncode}")
+    os.replace(tmp, out)
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    if force or not up_to_date():
+        _compile(nvcc_command(extra=("-Xptxas", "-v") if verbose else ()), LIB_PATH, verbose)
+    if force or not up_to_date(MARSHAL_PATH, (MARSHAL_SOURCE, os.path.join(INCLUDE, "fa_b200.h"))):
+        _compile(marshal_command(), MARSHAL_PATH, verbose)
     return LIB_PATH
 
 

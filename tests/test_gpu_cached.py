@@ -383,6 +383,60 @@ def test_prompt_then_tokens(cuda_device, d):
         n += T
 
 
+def test_python_refuses_what_does_not_fit(cuda_device):
+    cache = Cache([20, 30], 4, 2, 64, 16, seed=2)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k = _normal(g, 2, 4, 3, 64), _normal(g, 2, 2, 3, 64)
+    words = torch.ones(2, 3, dtype=torch.int64, device="cuda")
+    src, count = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    ws = torch.empty(fa.fa_cached_workspace_bytes(2, 4, 2, 3, 64), dtype=torch.uint8, device="cuda")
+    good = dict(q=q, k_pages=cache.k, v_pages=cache.v, page_table=cache.table, ctx_len=cache.ctx_len, tree=words,
+                workspace=ws)
+    fa.cached_attention(**good)
+    wide = torch.zeros(2, 4, 3, 128, dtype=torch.bfloat16, device="cuda")
+    for name, bad in (("q", q.float()), ("q", q.cpu()), ("q", q[0]), ("q", wide[..., ::2]), ("q", q[:1]),
+                      ("k_pages", cache.k.float()), ("k_pages", cache.k[0]), ("v_pages", cache.v[:1]),
+                      ("v_pages", cache.v.cpu()), ("v_pages", cache.v.transpose(2, 3)), ("page_table", cache.table.long()),
+                      ("page_table", cache.table[0]), ("page_table", cache.table.t()), ("ctx_len", cache.ctx_len[:1]),
+                      ("ctx_len", cache.ctx_len.cpu()), ("tree", words[:, :2]), ("tree", words.int()),
+                      ("workspace", ws.float()), ("workspace", ws.view(1, -1))):
+        with pytest.raises(ValueError):
+            fa.cached_attention(**{**good, name: bad})
+    for name in ("q", "k_pages", "v_pages", "page_table", "ctx_len", "tree", "workspace"):
+        with pytest.raises(TypeError):
+            fa.cached_attention(**{**good, name: 3})
+    for kw in (dict(window=0), dict(window=2**31), dict(sinks=-1), dict(sinks=2**40)):
+        with pytest.raises(ValueError):
+            fa.cached_attention(**good, **kw)
+    for kw in (dict(window=1.5), dict(window=None), dict(beta="2")):
+        with pytest.raises(TypeError):
+            fa.cached_attention(**good, **kw)
+    for kw in (dict(softmax_mode=7), dict(softmax_mode=2**40), dict(beta=1.0), dict(beta=math.inf)):
+        with pytest.raises(fa.FaError) as e:
+            fa.cached_attention(**good, **kw)
+        assert e.value.code == _abi.FA_ERR_INVALID_ARG
+    with pytest.raises(fa.FaError) as e:
+        fa.cached_attention(**{**good, "workspace": ws[:-1]})
+    assert e.value.code == _abi.FA_ERR_WORKSPACE
+    with pytest.raises(fa.FaError) as e:  # more than 64 new tokens
+        fa.cached_attention(_normal(g, 2, 4, 65, 64), cache.k, cache.v, cache.table, cache.ctx_len)
+    assert e.value.code == _abi.FA_ERR_UNSUPPORTED
+    for args in ((k, k[:, :, :2], None), (k.float(), k, None), (k, k, count.long()), (k, k, count[:1]), (q, q, None)):
+        with pytest.raises(ValueError):
+            fa.fa_cache_append(args[0], args[1], cache.k, cache.v, cache.table, cache.ctx_len, args[2])
+    for args in ((src.long(), count), (src[:1], count), (src, count[:1]), (src[0], count)):
+        with pytest.raises(ValueError):
+            fa.fa_cache_compact(cache.k, cache.v, cache.table, cache.ctx_len, *args)
+    with pytest.raises(ValueError):
+        fa.fa_cached_fwd(q, cache.k, cache.v, cache.table, cache.ctx_len, None, q[:, :2], torch.empty(2, 4, 3, device="cuda"), ws)
+    with pytest.raises(ValueError):
+        fa.fa_cached_fwd(q, cache.k, cache.v, cache.table, cache.ctx_len, None, q, torch.empty(2, 4, 3), ws)
+    # nothing to do, and a full pool of arguments all the same
+    o, lse = fa.cached_attention(q[:, :, :0], cache.k, cache.v, cache.table, cache.ctx_len)
+    assert o.shape == (2, 4, 0, 64) and lse.shape == (2, 4, 0)
+    assert fa.fa_device_error() == (0, 0)
+
+
 @pytest.mark.parametrize("T,H,Hkv,d", [(1, 2, 1, 64), (9, 4, 1, 128), (64, 2, 1, 128), (48, 8, 1, 64)])
 def test_withheld_arrive_ends_in_timeout(cuda_device, T, H, Hkv, d):
     """The bounded-wait exit of the split kernel in each of its forms (four, two and one copies of the rows, pairs of row

@@ -200,6 +200,55 @@ def test_streams_and_graph(cuda_device, d):
         assert (got[4].float() - ref[4].float()).abs().max() <= 2 * 2.0 ** -8 * ref[4].float().abs().max()
 
 
+def test_python_refuses_what_does_not_fit(cuda_device):
+    q, k, v, do = _inputs(1, 4, 2, 70, 64)
+    o, lse, st = fa.window_attention_forward(q, k, v, 8, 1)
+    for args in ((q.float(), k, v), (q.cpu(), k, v), (q[0], k, v), (q, k[:, :, :9], v), (q, k, v[:, :1]), (q, k.float(), v),
+                 (q, k, v.cpu()), (q.transpose(2, 3), k, v), (q, k[0], v)):
+        with pytest.raises(ValueError):
+            fa.window_attention_forward(*args, 8, 1)
+        with pytest.raises(ValueError):
+            fa.window_attention_backward(*args, o, do, lse, st.m, 8, 1)
+    for i in range(3):
+        args = [q, k, v]
+        args[i] = "x"
+        with pytest.raises(TypeError):
+            fa.window_attention_forward(*args, 8, 1)
+    for bad in (lse[:, :2], lse.half(), lse.cpu(), lse.transpose(1, 2)):
+        with pytest.raises(ValueError):
+            fa.fa_window_fwd(q, k, v, o, bad, None, 8, 1)
+        with pytest.raises(ValueError):
+            fa.window_attention_backward(q, k, v, o, do, bad, st.m, 8, 1)
+        with pytest.raises(ValueError):
+            fa.window_attention_backward(q, k, v, o, do, lse, bad, 8, 1)
+        with pytest.raises(ValueError):
+            fa.fa_window_fwd(q, k, v, o, lse, fa.RowStats(m=bad), 8, 1)
+    with pytest.raises(ValueError):
+        fa.fa_window_fwd(q, k, v, o, lse, fa.RowStats(rs=lse), 8, 1)
+    for window, sinks in ((0, 0), (-1, 0), (2**31, 0), (2**32 + 5, 0), (4, -1), (4, 2**31)):
+        with pytest.raises(ValueError):
+            fa.window_attention_forward(q, k, v, window, sinks)
+    for kw in (dict(softmax_mode=9), dict(beta=1.0), dict(beta=float("nan"))):
+        with pytest.raises(fa.FaError):
+            fa.window_attention_forward(q, k, v, 8, 1, **kw)
+    with pytest.raises(fa.FaError) as e:
+        fa.window_attention_backward(q, k, v, o, do, lse, None, 8, 1)  # a stabilised mode without its shift
+    assert e.value.code == 1
+    with pytest.raises(fa.FaError) as e:
+        fa.window_attention_backward(q, k, v, o, do, lse, st.m, 8, 1, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == 3
+    with pytest.raises(fa.FaError):  # a broadcast input: elements share memory
+        fa.window_attention_forward(q, k[:, :1].expand(1, 2, 70, 64), v, 8, 1)
+    o0, lse0, _ = fa.window_attention_forward(q[:, :, :0], k[:, :, :0], v[:, :, :0], 8, 1)
+    assert o0.numel() == 0 and lse0.shape == (1, 4, 0)
+    # partial statistics, and inputs that require gradients (the call records none)
+    m = torch.empty(1, 4, 70, device="cuda")
+    fa.fa_window_fwd(q, k, v, o, lse, fa.RowStats(m=m), 8, 1)
+    assert torch.equal(m, st.m)
+    o1, _, _ = fa.window_attention_forward(q.clone().requires_grad_(), k, v, 8, 1)
+    assert torch.equal(o1, o) and not o1.requires_grad
+
+
 def test_past_two_to_the_31_elements(cuda_device):
     """Tensors of more than 2^31 elements: the last rows of the last head, whose window reaches only their neighbours,
     against the formulas on a slice."""
