@@ -46,20 +46,16 @@ namespace fa {
 // (two per SM, 80 registers x 384 threads each), so with programmatic
 // dependent launch they are resident when the forward ends (measured: g2s
 // step 123.0 -> 122.4 us, long 2415 -> 2392 us, against 256-thread blocks).
-// The clear does not depend on the forward: the first clear_blocks blocks
-// zero one contiguous share of the accumulator each before they wait for the
-// forward grid.  When the accumulator is small (a quarter of L2 at most) the
-// host makes that one block per SM, the blocks resident beside the forward's
-// CTAs, so the whole clear runs while the forward does (g2s step 116.7 ->
-// 115.7 us); a larger one is shared by every block, since clearing it beside
-// the forward would push the forward's K and V tiles out of L2 (long: 2546
-// against 2373 us).  Against clearing each block's rows in the dot loop the
-// shared form took the g2s step from 123.1 to 121.3 us and long from 2396 to
-// 2373 us.  In the same place each
+// Each block also zeroes one contiguous share of the accumulator.  Nothing of
+// it before the dependency wait: the workspace may be memory that an earlier
+// call on the stream still reads or writes (one scratch tensor for several
+// calls; a block that a stream-ordered allocator hands on), and every kernel of
+// this library may let its dependents launch while it works.  Clearing before
+// the wait would save 2 us of the g2s step (115.7 against 117.7 us).  The
+// clear comes after the dot products, whose loads have the longer way (as
+// fast as before them on g2s, long 1 % faster in the windowed form).  Before the wait each
 // block asks for its share of dO to be brought into L2 (neutral on g2s and
-// tiestress, long step ~2420 -> ~2375 us over three runs).  The one kernel of this
-// library that reads the accumulator, the dQ convert of an earlier call, lets
-// its dependents start only after its last read.
+// tiestress, long step ~2420 -> ~2375 us over three runs).
 // 8 consecutive elements of O as they sit in memory (16 bytes of bf16 or
 // 32 bytes of fp32), and their dot product with 8 bf16 elements of dO
 template <typename OT>
@@ -110,7 +106,7 @@ struct ORaw<float> {
 template <int D, typename OT>
 __global__ void __launch_bounds__(128, 16)
 fa_bwd_delta_kernel(const OT* __restrict__ o, const __nv_bfloat16* __restrict__ dO,
-                    float* __restrict__ delta, float* __restrict__ dq_acc, long long rows, int clear_blocks) {
+                    float* __restrict__ delta, float* __restrict__ dq_acc, long long rows) {
   constexpr int LPR = D / 8;               // lanes per row (8 elements per lane)
   constexpr int RPW = 32 / LPR;            // rows per warp per group
   constexpr int U = 2;                     // row groups per warp per pass
@@ -118,16 +114,8 @@ fa_bwd_delta_kernel(const OT* __restrict__ o, const __nv_bfloat16* __restrict__ 
   const long long warp_global = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const long long n_warps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
   const int sub = lane / LPR, li = lane % LPR;
-  if (static_cast<int>(blockIdx.x) < clear_blocks) {
-    const long long n4 = rows * (D / 4);
-    const long long lo = n4 * blockIdx.x / clear_blocks, hi = n4 * (blockIdx.x + 1) / clear_blocks;
-    float4* acc4 = reinterpret_cast<float4*>(dq_acc);
-    for (long long i = lo + threadIdx.x; i < hi; i += blockDim.x) acc4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    // the 256-byte block after the accumulator (the d = 128 kernel's work-item counter)
-    if (blockIdx.x == 0 && threadIdx.x < 64) reinterpret_cast<unsigned int*>(dq_acc + rows * D)[threadIdx.x] = 0u;
-  }
-  // and its share of dO into L2 (a prefetch is only a hint, so it is harmless
-  // even if the previous grid is still writing dO)
+  // this block's share of dO into L2 (a prefetch is only a hint, so it is
+  // harmless even if the previous grid is still writing dO)
   if (threadIdx.x == 0) {
     const long long nb = rows * D * 2;  // bytes of dO; its base is 16-byte aligned (checked by its tensor map)
     const long long lo = (nb * blockIdx.x / gridDim.x) & ~15ll;
@@ -167,6 +155,12 @@ fa_bwd_delta_kernel(const OT* __restrict__ o, const __nv_bfloat16* __restrict__ 
       if (r < rows && li == 0) delta[r] = acc;
     }
   }
+  const long long n4 = rows * (D / 4);
+  const long long lo = n4 * blockIdx.x / gridDim.x, hi = n4 * (blockIdx.x + 1) / gridDim.x;
+  float4* acc4 = reinterpret_cast<float4*>(dq_acc);
+  for (long long i = lo + threadIdx.x; i < hi; i += blockDim.x) acc4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // the 256-byte block after the accumulator (the d = 128 kernel's work-item counter)
+  if (blockIdx.x == 0 && threadIdx.x < 64) reinterpret_cast<unsigned int*>(dq_acc + rows * D)[threadIdx.x] = 0u;
 }
 
 // --------------------------------------------------------------- dQ convert
@@ -201,9 +195,6 @@ fa_bwd_dq_convert_kernel(const float* __restrict__ dq_acc, __nv_bfloat16* __rest
       }
     }
   }
-  // the delta kernel of a later call clears the accumulator before its own
-  // dependency wait: let it start only once every read here has been used
-  __syncthreads();
   grid_launch_dependents();
 }
 

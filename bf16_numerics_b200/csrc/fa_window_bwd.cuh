@@ -10,25 +10,20 @@
 
 namespace fa {
 
-// delta[(b*H + h)*N + n] = sum_c dO * O in fp32.  The first clear_blocks blocks
-// zero `clear4` float4 starting at `clear` (the dQ accumulator and what
-// follows it) before they wait for the grid ahead: see fa_bwd_delta_kernel for
-// how the host picks their number and why dependents launch only after the
-// wait.
+// delta[(b*H + h)*N + n] = sum_c dO * O in fp32, and `clear4` float4 starting at
+// `clear` (the dQ accumulator and what follows it) zeroed: see
+// fa_bwd_delta_kernel for why that comes last and why dependents launch only
+// after the wait.
 template <int D>
 __global__ void __launch_bounds__(128, 16)
 fa_window_delta_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dO, ViewStrides so,
                        ViewStrides sdo, float* __restrict__ delta, float4* __restrict__ clear, long long clear4, int H,
-                       int N, long long groups, int groups_per_head, int clear_blocks) {
+                       int N, long long groups, int groups_per_head) {
   constexpr int LPR = D / 8;     // lanes per row (8 elements per lane)
   constexpr int RPW = 32 / LPR;  // rows per warp per pass
   constexpr int U = 2;           // passes per group: RPW * U rows, all loads before any use
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, li = lane % LPR;
-  if (static_cast<int>(blockIdx.x) < clear_blocks) {
-    const long long lo = clear4 * blockIdx.x / clear_blocks, hi = clear4 * (blockIdx.x + 1) / clear_blocks;
-    for (long long i = lo + threadIdx.x; i < hi; i += blockDim.x) clear[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
   grid_dependency_wait();  // O comes from the forward grid
   grid_launch_dependents();
   const long long warp_global = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -62,6 +57,8 @@ fa_window_delta_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16*
       if (n < N && li == 0) delta[bh * N + n] = acc;
     }
   }
+  const long long lo = clear4 * blockIdx.x / gridDim.x, hi = clear4 * (blockIdx.x + 1) / gridDim.x;
+  for (long long i = lo + threadIdx.x; i < hi; i += blockDim.x) clear[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 // dq = bf16(dq_acc), and dk, dv of the key blocks that were worked on in pieces
@@ -148,9 +145,6 @@ fa_window_convert_kernel(const ConvertParams p) {
       }
     }
   }
-  // a later call's delta kernel clears the accumulator before its own
-  // dependency wait: let it start only once every read here has been used
-  __syncthreads();
   grid_launch_dependents();
 }
 

@@ -235,12 +235,11 @@ fa_status launch_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v
     const long long groups = static_cast<long long>(BH) * per_head;
     const long long clear4 = static_cast<long long>(wl.part_off - wl.acc_off) / 16;
     const dim3 grid(grid_for(groups, 4));
-    const int clear_blocks = delta_clear_blocks(static_cast<int>(grid.x), clear4 * 16);
     LaunchTimer tm(FA_KERNEL_BWD_DELTA, stream);
     cudaError_t e = launch_pdl(fa::fa_window_delta_kernel<D>, grid, dim3(128), 0, stream,
                                static_cast<const __nv_bfloat16*>(o->ptr), static_cast<const __nv_bfloat16*>(dO->ptr),
                                strides_of(o), strides_of(dO), delta, reinterpret_cast<float4*>(dq_acc), clear4, H, N,
-                               groups, per_head, clear_blocks);
+                               groups, per_head);
     tm.done();
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail("fa_window_delta_kernel launch", e);
