@@ -49,7 +49,8 @@
 // after the other.  With few rows the loads bind: 64 sequences to 8192, 16 heads
 // over 4, d = 128 (675 MB): 119 us, of which 105 at 6.4 TB/s.
 //   TMEM: S_t [128t, 128t+128), P_bar_t over its first 64 columns, O_t at 256 + D t.
-// Pages that no row sees are not read (their place is filled with zeros by an
+// Pages that no row sees -- behind the window, or of absent tokens alone that no
+// word names -- are not read (their place is filled with zeros by an
 // out-of-range box); what lies in a read page behind the last token, or in the
 // slot of an absent token, may be anything: its scores are masked and its V
 // rows are overwritten with zeros in shared memory (0 * NaN would not be 0).
@@ -339,13 +340,37 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     // -------------------------------------------------------------- TMA producer
     const int rows = p.page < 128 ? p.page : 128;  // rows of a box
     const int boxes = 128 / rows;                  // boxes per tile: one lane each
+    // what the rows of the current sequence see of it: the new tokens that a
+    // word names (0: no row sees anything), and the first context slot in the
+    // window of the row that reaches back furthest -- the one that sees the fewest
+    // new tokens, which need not be the root: that one may be absent
+    unsigned long long named = 0ull;
+    int near = 0;
+    auto look = [&](const CachedCursor& c) {
+      const unsigned long long all_new = p.T == 64 ? ~0ull : (1ull << p.T) - 1ull;
+      int fewest = 1;
+      named = all_new;
+      if (p.tree != nullptr) {
+        const unsigned long long* words = p.tree + static_cast<long long>(c.b) * p.T;
+        const unsigned long long w0 = lane < p.T ? __ldg(words + lane) & all_new : 0ull;
+        const unsigned long long w1 = lane + 32 < p.T ? __ldg(words + lane + 32) & all_new : 0ull;
+        const unsigned long long w = w0 | w1;
+        named = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(w)) |
+                static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(w >> 32))) << 32;
+        const unsigned n0 = w0 ? __popcll(w0) : 65, n1 = w1 ? __popcll(w1) : 65;
+        fewest = static_cast<int>(__reduce_min_sync(0xffffffffu, n0 < n1 ? n0 : n1));
+      }
+      near = c.seq.ctx + fewest - p.window;
+    };
     // page of this lane's box in tile i of the segment (num_pages, out of
     // range: the box is filled with zeros)
     auto page_of = [&](const CachedCursor& c, int i) -> int {
       if (lane >= boxes) return 0;
-      const int first = c.seq.tile(c.i0 + i) * 128 + lane * rows;  // first slot
-      const bool seen = first < c.seq.total &&
-                        (first + rows > c.seq.ctx || first + rows > c.seq.ctx - p.window + 1 || first < p.sinks);
+      const int ctx = c.seq.ctx, first = c.seq.tile(c.i0 + i) * 128 + lane * rows;  // first slot
+      if (first >= c.seq.total || named == 0ull) return p.num_pages;
+      bool seen = first < ctx && (first < p.sinks || (ctx - first < rows ? ctx : first + rows) > near);
+      const int u0 = first > ctx ? first - ctx : 0, n = rows - (ctx > first ? ctx - first : 0);  // new tokens [u0, u0 + n)
+      if (n > 0 && u0 < 64) seen = seen || ((named >> u0) & (n < 64 ? (1ull << n) - 1ull : ~0ull)) != 0ull;
       if (!seen) return p.num_pages;
       const int id = __ldg(p.table + static_cast<long long>(c.b) * p.width + first / p.page);
       if (id < 0 || id >= p.num_pages) {
@@ -371,8 +396,10 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       ++issued;
       return true;
     };
-    for (; ok && cur.valid(); cur.next(p)) {
+    for (int b = -1; ok && cur.valid(); cur.next(p)) {
       const int hk = cur.key_head(p);
+      if (cur.b != b) look(cur);
+      b = cur.b;
       int id = page_of(cur, 0);
       for (int i = 0; i < cur.n; ++i) {
         const int tile = cur.seq.tile(cur.i0 + i);
