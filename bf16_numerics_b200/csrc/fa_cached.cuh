@@ -359,8 +359,9 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(w >> 32))) << 32;
         const unsigned n0 = w0 ? __popcll(w0) : 65, n1 = w1 ? __popcll(w1) : 65;
         fewest = static_cast<int>(__reduce_min_sync(0xffffffffu, n0 < n1 ? n0 : n1));
+        if (named == 0ull) fewest = 1;
       }
-      near = c.seq.ctx + fewest - p.window;
+      near = window_first(c.seq.ctx, fewest, p.window);
     };
     // page of this lane's box in tile i of the segment (num_pages, out of
     // range: the box is filled with zeros)
@@ -543,7 +544,6 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int ctx = cur.seq.ctx, n = cur.n;
     // this row's new tokens, and the union over the rows (which slots hold one)
     unsigned long long bits = 0ull, any = 0ull;
-    int lo = 0;
     if (p.tree == nullptr) {
       bits = (2ull << tok) - 1ull;  // tok = 63: all ones
       any = all_new;
@@ -558,7 +558,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       bits = __ldg(words + tok) & all_new;
     }
     const bool absent = bits == 0ull;  // works like a row that sees the context; its result is put down as empty
-    lo = ctx + __popcll(bits) - p.window;  // first key of the window (pos - window + 1)
+    const int lo = window_first(ctx, __popcll(bits), p.window);
     if (p.window <= p.T && !absent) {
       // some new tokens may be out of the window too (positions of new tokens are
       // in [ctx - 1, ctx + T): an absent one's is ctx - 1)
@@ -592,8 +592,8 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int c = 0; c < CW; ++c) x[c] = __uint_as_float(raw[c]);
       }
       const int key0 = kv0 + col;  // slot of x[0]
-      if (__any_sync(0xffffffffu, key0 + CW > ctx || (key0 < lo && key0 + CW > p.sinks))) {
-        const RowMask mk{lo - key0, ctx - key0, p.sinks - key0};
+      if (__any_sync(0xffffffffu, context_hides(ctx, lo, p.sinks, key0, CW))) {
+        const RowMask mk = context_mask(ctx, lo, p.sinks, key0);
 #pragma unroll
         for (int w = 0; w < CW / 32; ++w) {
           uint32_t vis = mk.word(32 * w);
@@ -717,7 +717,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       l += psum;
       // V rows of slots that hold no token: zeros (the tile's own slot r; PAIR:
       // slot 0 does it, whose product comes first)
-      if (kv0 + 128 > ctx && (!PAIR || t == 0)) {
+      if (ctx - kv0 < 128 && (!PAIR || t == 0)) {
         const int s = (g0 + i) % L::VS, u = kv0 + r - ctx;
         ok = wait.warp(bar(L::V_FULL + s), ((g0 + i) / L::VS) & 1, 12);
         if (!ok) continue;

@@ -37,6 +37,23 @@ struct RowMask {
   }
 };
 
+// Over a cache: the first context slot in the window of a new token that sees
+// n of the new tokens, itself included (so it stands at ctx + n - 1); ctx + n
+// and the window are below 2^31.  Not below slot 0: with a window of 2^31 - 1 the
+// difference to a far slot would not fit.
+__device__ __forceinline__ int window_first(int ctx, int n, int window) {
+  const int first = ctx + n - window;
+  return first > 0 ? first : 0;
+}
+// .. and how it sees the context in slots [key0, ..): not where key0 is beyond ctx
+__device__ __forceinline__ RowMask context_mask(int ctx, int first, int sinks, int key0) {
+  return RowMask{first - key0, ctx - key0, sinks - key0};
+}
+// whether n slots from key0 on hold any that it may not see
+__device__ __forceinline__ bool context_hides(int ctx, int first, int sinks, int key0, int n) {
+  return ctx - key0 < n || (key0 < first && sinks - key0 < n);
+}
+
 struct WindowShape {
   int H, G;            // query heads, query heads per key head
   int window, sinks;   // 1 <= window <= N, 0 <= sinks <= N (the host clips both)
