@@ -4,9 +4,10 @@ Thin marshalling layer over the C ABI of ``libfa_b200.so`` (include/fa_b200.h).
 Every function with an ``fa_`` name maps 1:1 to the C entry point of the same
 name; tensors are passed as device pointers, the stream as the CUDA stream
 handle.  The windowed and the cached calls, which a model makes per layer and
-token, are marshalled in C++ (csrc/fa_torch.cpp), the others with ctypes.  PyTorch only provides device memory and streams.  There is no CPU or
-library fallback: if the CUDA library is missing, importing the entry points
-raises.
+token, are marshalled in C++ (csrc/fa_torch.cpp), the others with ctypes.
+PyTorch only provides device memory and streams.  There is no CPU or library
+fallback: if the CUDA library, or the marshalling module of the running torch,
+is missing, the first call that needs it raises ImportError.
 
 Method: Qiu & Yao, "Why Low-Precision Transformer Training Fails: An Analysis
 on Flash Attention" (arXiv 2510.04212) -- the safe softmax P_bar = exp(S - m)

@@ -118,14 +118,21 @@ _bound = None
 
 
 def marshal():
-    """The C++ marshalling module, bound to the loaded library."""
+    """The C++ marshalling module of this Python and torch, bound to the loaded library."""
     global _bound
     if _bound is None:
-        lib = load()
-        from . import _marshal
+        import importlib.util
 
-        _marshal.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in MARSHALLED))
-        _bound = _marshal
+        from .build import marshal_path
+
+        lib, path = load(), marshal_path()
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python -m bf16_numerics_b200.build`")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._marshal", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in MARSHALLED))
+        _bound = module
     return _bound
 
 

@@ -4,8 +4,11 @@
 
 The library is a single translation unit (csrc/fa_lib.cu) that includes the
 kernel headers; the CUDA runtime is linked statically so the library does not
-depend on the runtime version PyTorch ships.  _marshal.so (csrc/fa_torch.cpp,
-g++) turns torch tensors into calls of the library.
+depend on the runtime version PyTorch ships.  The marshalling module
+(csrc/fa_torch.cpp, g++) turns torch tensors into calls of the library; it is
+bound to the C++ ABI of one torch and the C API of one Python, which its file
+name therefore carries: another torch in the same tree finds none of its own
+and builds one.
 """
 
 from __future__ import annotations
@@ -22,14 +25,23 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libfa_b200.so")
 SOURCES = [os.path.join(CSRC, "fa_lib.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
-    os.path.join(INCLUDE, "fa_b200.h")]
+    os.path.join(INCLUDE, "fa_b200.h"), os.path.abspath(__file__)]
 
-
-MARSHAL_PATH = os.path.join(PKG_DIR, "_marshal.so")
 MARSHAL_SOURCE = os.path.join(CSRC, "fa_torch.cpp")
+MARSHAL_DEPS = [MARSHAL_SOURCE, os.path.join(INCLUDE, "fa_b200.h"), os.path.abspath(__file__)]
 
 
-def marshal_command(out: str = MARSHAL_PATH) -> list[str]:
+def marshal_path() -> str:
+    """The marshalling module of the running Python and torch."""
+    import sysconfig
+
+    import torch
+
+    abi = f"{sysconfig.get_config_var('SOABI')}-torch-{torch.__version__}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(PKG_DIR, f"_marshal.{abi}.so")
+
+
+def marshal_command(out: str) -> list[str]:
     import sysconfig
 
     import torch
@@ -77,8 +89,9 @@ def _compile(cmd: list[str], out: str, verbose: bool) -> None:
 def build_library(force: bool = False, verbose: bool = False) -> str:
     if force or not up_to_date():
         _compile(nvcc_command(extra=("-Xptxas", "-v") if verbose else ()), LIB_PATH, verbose)
-    if force or not up_to_date(MARSHAL_PATH, (MARSHAL_SOURCE, os.path.join(INCLUDE, "fa_b200.h"))):
-        _compile(marshal_command(), MARSHAL_PATH, verbose)
+    marshal = marshal_path()
+    if force or not up_to_date(marshal, MARSHAL_DEPS):
+        _compile(marshal_command(marshal), marshal, verbose)
     return LIB_PATH
 
 
