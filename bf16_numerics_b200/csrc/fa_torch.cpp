@@ -209,10 +209,10 @@ PyObject* window_forward(PyObject* const* a) {
   view("q", a[0], s.q, s.dev);
   Tensor o = at::empty_like(q), lse = floats(s.rows, s.dev);
   if (a[7] != Py_True) return result(window_fwd_call(s, a, view_of(o), lse.data_ptr<float>(), nullptr, x), o, lse);
-  // the four statistics in one allocation
-  const int64_t all[4] = {4, s.rows[0], s.rows[1], s.rows[2]};
-  Tensor rows = floats(all, s.dev);
-  Tensor rm = rows.select(0, 0), rs = rows.select(0, 1).view(at::kInt), m = rows.select(0, 2), pbar = rows.select(0, 3);
+  // m, which the backward needs, on its own; the others in one allocation
+  const int64_t all[4] = {3, s.rows[0], s.rows[1], s.rows[2]};
+  Tensor rows = floats(all, s.dev), m = floats(s.rows, s.dev);
+  Tensor rm = rows.select(0, 0), rs = rows.select(0, 1).view(at::kInt), pbar = rows.select(0, 2);
   const fa_row_stats st{rm.data_ptr<float>(), rs.data_ptr<int32_t>(), m.data_ptr<float>(), pbar.data_ptr<float>()};
   return result(window_fwd_call(s, a, view_of(o), lse.data_ptr<float>(), &st, x), o, lse, rm, rs, m, pbar);
 }
