@@ -260,6 +260,8 @@ def _call(stream, device_of, name, *args):
     call = getattr(_abi.marshal(), name)
     if stream is None:
         return call(*args)
+    if not isinstance(device_of, torch.Tensor):
+        raise TypeError("the first argument must be a torch.Tensor")
     if stream.device != device_of.device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device_of.device}")
     with torch.cuda.stream(stream):
