@@ -43,11 +43,15 @@
 // us so).  One warp loads (TMA: K and V through rings, one box per page, so a page
 // may lie anywhere and be smaller than a tile), one issues products.
 //
-// Measured there: a row tile's step takes ~3600 cycles where its products need
-// 1024 -- scores from TMEM, maximum and ties 950, exponentials 1500, P_bar and the
-// rescale of O 700-950, then P V and the next S 1400 in the issuing thread, one
-// after the other.  With few rows the loads bind: 64 sequences to 8192, 16 heads
-// over 4, d = 128 (675 MB): 119 us, of which 105 at 6.4 TB/s.
+// What bounds the full row tiles (the same case at 142 us): a step of a pair -- one
+// 128-key tile for both row tiles -- takes 5300 cycles where its four products need
+// 2048.  Clock stamps of one softmax thread in a copy of the kernel (5600 cycles a
+// step with them): 2000 waiting for its scores (the slot's P V and next S, behind
+// the other slot's), 1300 maximum, ties and the exchange of the halves, 1350
+// exponentials, 230 waiting for O, 480 rescale, 250 reading scores and handing P_bar
+// over.  These instances (two warpgroups per slot) also spill, about 300 bytes of
+// stores and 400 of loads a thread.  With few rows the loads bind: 64 sequences to
+// 8192, 16 heads over 4, d = 128 (675 MB): 119 us, of which 105 at 6.4 TB/s.
 //   TMEM: S_t [128t, 128t+128), P_bar_t over its first 64 columns, O_t at 256 + D t.
 // Pages that no row sees -- behind the window, or of absent tokens alone that no
 // word names -- are not read (their place is filled with zeros by an

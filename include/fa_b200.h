@@ -30,6 +30,13 @@
  *   P_bar = exp(S - m),  l = rowsum(P_bar),  P = P_bar / l,  O = P V
  *   lse   = m + ln(l)                          (natural logarithm)
  *
+ * On a tied maximum the rule moves the shift by |rm| (beta - 1) or |rm|.  The
+ * kernels apply it to the running maximum as they walk through a row's keys
+ * (fa_cached_fwd: through each part's): with beta = 2 a row that meets a tied
+ * maximum beyond about 80 in size on the way, the final one or not, underflows
+ * in fp32, and its outputs are wrong or NaN.  FA_SOFTMAX_STANDARD has no such
+ * limit.
+ *
  *   backward: delta = rowsum(dO o O), dV = P^T dO, dP = dO V^T,
  *             dS = P o (dP - delta), dQ = dS K * scale, dK = dS^T Q * scale,
  *   with P recomputed as exp(S - lse) (standard) or as
@@ -220,8 +227,6 @@ fa_status fa_window_bwd(const fa_view* q, const fa_view* k, const fa_view* v, co
  * slot need not have been written unless another token's word names it.  window >= 1 (2^31 - 1: no window), sinks
  * >= 0.  Softmax modes as in fa_fwd; the context is processed in parts that are
  * joined at the end, and the shift rule applies to the keys of each part.
- * With tied maxima the rule moves the shift by |rm| (beta - 1) or |rm|: as in
- * fa_fwd, rows with a tied maximum beyond about 80 in size underflow.
  *
  * Slots below ctx_len[b] of a page any slot of which is visible, and the slots
  * of tokens that are not absent, hold finite values; anything may lie in other
