@@ -51,11 +51,13 @@ namespace fa {
 // call on the stream still reads or writes (one scratch tensor for several
 // calls; a block that a stream-ordered allocator hands on), and every kernel of
 // this library may let its dependents launch while it works.  Clearing before
-// the wait would save 2 us of the g2s step (115.7 against 117.7 us).  The
-// clear comes after the dot products, whose loads have the longer way (as
-// fast as before them on g2s, long 1 % faster in the windowed form).  Before the wait each
-// block asks for its share of dO to be brought into L2 (neutral on g2s and
-// tiestress, long step ~2420 -> ~2375 us over three runs).
+// the wait, beside the forward, would save 2 us of the g2s step (115.7 against
+// 117.7 us) and 5 of the windowed one (B8 H12 N1024 d64, window 256: 111.6
+// against 116.4 us).  The clear comes after the dot products, whose loads have
+// the longer way: as fast as before them on g2s, 1 % faster on 2 x 16 heads over 4,
+// N 8192, d 128, window 1024.  Before the wait each block only asks for its share
+// of dO to be brought into L2 (neutral on g2s and tiestress, long step ~2420 ->
+// ~2375 us over three runs).
 // 8 consecutive elements of O as they sit in memory (16 bytes of bf16 or
 // 32 bytes of fp32), and their dot product with 8 bf16 elements of dO
 template <typename OT>
